@@ -112,7 +112,8 @@ int tq_device_status(int32_t *flags_out, int clear);
  *   down launch of the smallest batches, 6 route_unpermute, 7 trellis_decode, 8 trellis_gemv,
  *   9 GEMM gate/up+SiLU, 10 GEMM down, 11 GEMM preparation (tile list, route-ordered
  *   activation rows), 12 GEMV activation quantisation (x' rows to 16-bit fixed point),
- *   13 trellis_encode, 14 route_gather_rows.
+ *   13 trellis_encode, 14 route_gather_rows, 15 swiglu_forward, 16 swiglu_backward,
+ *   17 fp8_block_quantize / _dequantize, 18 the product of fp8_block_gemm / _linear.
  * tq_profile_enable creates 2*max_launches events (host-side CUDA resources; call it
  * outside graph capture); launches beyond max_launches are not recorded.  A launch made
  * during stream capture records its events as external event-record nodes of the graph,
@@ -302,6 +303,91 @@ int route_unpermute_signed(const float *y_perm, const int32_t *inv, const float 
 size_t trellis_encode_workspace_size(int K, int rows, int cols);
 int trellis_encode(const float *target, int K, int rows, int cols, uint32_t *bits,
                    uint32_t *tile_cost, void *ws, size_t ws_bytes, tq_stream stream);
+
+/*
+ * The dense expert: the gated feed-forward block and the 8-bit product of an expert that
+ * every token uses, next to the routed ones (no counterpart on the pages, whose subject is
+ * the routed experts).  Matrices are row-major and packed; a weight is [outputs][inputs].
+ *
+ * fp8_block_quantize -- x stored as E4M3 with one scale for each block of block_rows x 128
+ * values (block_rows 1: rows of activations; 128: weights).  Blocks start at multiples of
+ * block_rows and 128; the last ones may be smaller.  A block's scale is the power of two
+ * 2^e, e the smallest integer >= -126 with max|x| <= 448 * 2^e over the block's finite
+ * values (scale 1 for a block of zeros); q = E4M3(x * 2^-e), nearest even.  An infinity or
+ * NaN becomes the E4M3 NaN.  Deterministic: one rounding, no arithmetic that could differ.
+ *   x      : [rows][cols] of x_dtype (F16, BF16 or F32), 16-byte aligned.
+ *   out    : [rows][cols] E4M3 bytes.  scales : [ceil(rows / block_rows)][ceil(cols / 128)]
+ *            fp32.  Both 16-byte aligned.
+ *   cols % 8 == 0; block_rows is 1 or 128.
+ * fp8_block_dequantize -- out = q * scale in fp32, rounded once to out_dtype.
+ */
+int fp8_block_quantize(const void *x, int x_dtype, int64_t rows, int cols, int block_rows, uint8_t *out,
+                       float *scales, tq_stream stream);
+int fp8_block_dequantize(const uint8_t *q, const float *scales, int64_t rows, int cols, int block_rows,
+                         void *out, int out_dtype, tq_stream stream);
+
+/*
+ * fp8_block_gemm -- product of E4M3 matrices with a scale for each block of 128:
+ *   y[m][n] = sum_b s_x[m][b] * s_w[n / 128][b] * sum_{k in block b} x[m][k] * w[n][k]
+ * E4M3 products are exact; each block's sum is fp32 in tensor memory and is multiplied by
+ * s_x * s_w (any fp32 values) and added in fp32.
+ *   x : [M][K] E4M3, s_x : [M][ceil(K / 128)] fp32.
+ *   w : [N][K] E4M3, s_w : [ceil(N / 128)][ceil(K / 128)] fp32.
+ *   y : [M][N] of y_dtype (F16, BF16 or F32); accumulate != 0 (F32 only): y += the product.
+ *   K % 16 == 0; M and N any size; all arrays 16-byte aligned.
+ * fp8_block_linear -- the same from activations x [M][K] of x_dtype (F16, BF16 or F32),
+ * which are quantised as fp8_block_quantize (block_rows 1) does on the way.  ws: device
+ * workspace of fp8_block_linear_workspace_size(M, K) bytes, 16-byte aligned.
+ */
+int fp8_block_gemm(const uint8_t *x, const float *s_x, const uint8_t *w, const float *s_w, int M, int N, int K,
+                   void *y, int y_dtype, int accumulate, tq_stream stream);
+size_t fp8_block_linear_workspace_size(int M, int K);
+int fp8_block_linear(const void *x, int x_dtype, const uint8_t *w, const float *s_w, int M, int N, int K,
+                     void *y, int y_dtype, int accumulate, void *ws, size_t ws_bytes, tq_stream stream);
+
+/*
+ * A SwiGLU block's activations kept in 8 bits between its forward and backward pass (device
+ * arrays, E4M3 and scales as fp8_block_quantize with block_rows 1 writes them, 16-byte
+ * aligned): the input x [T][D] with s_x [T][ceil(D / 128)], and the projections before the
+ * activation g and u [T][F] with s_g and s_u [T][ceil(F / 128)].
+ */
+typedef struct {
+    uint8_t *x;
+    float *s_x;
+    uint8_t *g;
+    float *s_g;
+    uint8_t *u;
+    float *s_u;
+} tq_swiglu_saved;
+
+/*
+ * swiglu_forward -- h = silu(g) * u with g = x W_gate^T, u = x W_up^T, in one kernel (fp32
+ * sums; g and u are not rounded, h once).
+ *   x : [T][D], w_gate, w_up : [F][D], h : [T][F], all of dtype (F16 or BF16), 16-byte
+ *   aligned.  D % 8 == 0, F % 8 == 0.
+ *   saved: NULL, or the arrays that receive x, g and u in 8 bits (g and u are stored from
+ *   their fp32 sums by the same kernel); h is the same either way up to the order of its sums.
+ */
+int swiglu_forward(const void *x, const void *w_gate, const void *w_up, int dtype, int T, int D, int F,
+                   void *h, const tq_swiglu_saved *saved, tq_stream stream);
+
+/*
+ * swiglu_backward -- gradients of swiglu_forward for a gradient dh [T][F] of h:
+ *   dg = dh * u * s * (1 + g * (1 - s)), du = dh * g * s, s = 1 / (1 + e^-g);
+ *   dx = dg W_gate + du W_up,  dw_gate = dg^T x,  dw_up = du^T x
+ * from exactly one of x (g and u are computed again) and saved (x, g and u are the 8-bit
+ * values that swiglu_forward stored; dx, dw follow from those values).  The other is NULL.
+ * dg and du are rounded to bf16 for the products; sums are fp32.  Results are written (not
+ * added), do not depend on the order of execution, and must not overlap the inputs.
+ *   dtype: BF16 (F16: TQ_ERR_UNSUPPORTED, its range does not hold dg and du).
+ *   dx : [T][D], dw_gate, dw_up : [F][D].  ws: device workspace of
+ *   swiglu_backward_workspace_size(T, D, F, saved != NULL) bytes, 16-byte aligned.
+ *   T = 0 writes zero weight gradients.
+ */
+size_t swiglu_backward_workspace_size(int T, int D, int F, int from_saved);
+int swiglu_backward(const void *dh, const void *x, const tq_swiglu_saved *saved, const void *w_gate,
+                    const void *w_up, int dtype, int T, int D, int F, void *dx, void *dw_gate, void *dw_up,
+                    void *ws, size_t ws_bytes, tq_stream stream);
 
 /* One width group of a layer: experts of one K, concatenated in ascending global id. */
 typedef struct {

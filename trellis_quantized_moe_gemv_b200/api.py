@@ -45,6 +45,11 @@ class TqMoeLayer(ctypes.Structure):
 CODEBOOKS = {"t16": 0, "pair_e4m3": 1}
 
 
+class TqSwigluSaved(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in ("x", "s_x", "g", "s_g", "u", "s_u")]
+
+
+
 _lib = None
 _VP, _I, _I64, _SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
 
@@ -81,6 +86,15 @@ SIGNATURES = {
                           _SZ, _VP], _I),
     "moe_trellis_gemv_noalloc": ([ctypes.POINTER(TqMoeLayer), _VP, _VP, _VP, _VP, _VP, _I, _I, _VP,
                                   _VP], _I),
+    "fp8_block_quantize": ([_VP, _I, _I64, _I, _I, _VP, _VP, _VP], _I),
+    "fp8_block_dequantize": ([_VP, _VP, _I64, _I, _I, _VP, _I, _VP], _I),
+    "fp8_block_gemm": ([_VP, _VP, _VP, _VP, _I, _I, _I, _VP, _I, _I, _VP], _I),
+    "fp8_block_linear_workspace_size": ([_I, _I], _SZ),
+    "fp8_block_linear": ([_VP, _I, _VP, _VP, _I, _I, _I, _VP, _I, _I, _VP, _SZ, _VP], _I),
+    "swiglu_forward": ([_VP, _VP, _VP, _I, _I, _I, _I, _VP, ctypes.POINTER(TqSwigluSaved), _VP], _I),
+    "swiglu_backward_workspace_size": ([_I, _I, _I, _I], _SZ),
+    "swiglu_backward": ([_VP, _VP, ctypes.POINTER(TqSwigluSaved), _VP, _VP, _I, _I, _I, _I, _VP, _VP, _VP, _VP,
+                         _SZ, _VP], _I),
 }
 
 
@@ -152,7 +166,7 @@ def device_status(clear: bool = False) -> int:
 
 STAGES = ("route_topk", "route_permute", "rotate_x", "moe_gemv", "rotate_h", "gemv_down",
           "route_unpermute", "trellis_decode", "trellis_gemv", "gemm_gateup", "gemm_down", "gemm_prep",
-          "gemv_quant", "trellis_encode", "route_gather")
+          "gemv_quant", "trellis_encode", "route_gather", "swiglu", "swiglu_grad", "fp8_store", "fp8_gemm")
 
 
 def launch_count() -> int:
@@ -385,6 +399,235 @@ def route_unpermute_signed(y_perm: torch.Tensor, inv: torch.Tensor, topk_w: torc
     return out
 
 
+# ----------------------------------------------------------------------------- dense expert
+
+FP8 = torch.float8_e4m3fn
+BLOCK = 128     # values of one row (and, for weights, rows) under one scale
+
+
+def _blocks(n: int) -> int:
+    return -(-n // BLOCK)
+
+
+def _require_dense(t, dtype, shape, name):
+    """A contiguous CUDA tensor of this dtype (None: any the entry point takes) and shape, on
+    the current device, where the kernels run."""
+    _require(t, t.dtype if dtype is None and isinstance(t, torch.Tensor) else dtype, name)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError("%s is on %s, but the current device is cuda:%d" % (name, t.device, torch.cuda.current_device()))
+
+
+def _require_matrix(t, dtype, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a torch.Tensor" % name)
+    if t.dim() != 2:
+        raise ValueError("%s must be a matrix, got %d dimensions" % (name, t.dim()))
+    _require_dense(t, dtype, t.shape, name)
+    return t.shape
+
+
+def _new(shape, dtype, device, stream):
+    """An uninitialised tensor for a call on `stream` (None: the current stream).  Memory for
+    another stream comes from that stream's pool, so that nothing still running on the
+    current stream owns it, and is kept until the current stream's uses of it are over."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream())
+    return t
+
+
+def _out(out, shape, dtype, name, device, stream):
+    if out is None:
+        return _new(shape, dtype, device, stream)
+    _require_dense(out, dtype, shape, name)
+    return out
+
+
+def _workspace(ws, need, device, stream):
+    if ws is None:
+        return _new(max(need, 16), torch.uint8, device, stream)
+    if not isinstance(ws, torch.Tensor):
+        raise TypeError("ws must be a torch.Tensor")
+    _require_dense(ws, None, ws.shape, "ws")
+    return ws
+
+
+def _float_dtype(t, name):
+    if not isinstance(t, torch.Tensor) or t.dtype not in TQ_DTYPE:
+        raise TypeError("%s must be an fp16, bf16 or fp32 tensor" % name)
+    return TQ_DTYPE[t.dtype]
+
+
+def fp8_block_quantize(x: torch.Tensor, block_rows: int = 1, out: Optional[torch.Tensor] = None,
+                       scales: Optional[torch.Tensor] = None, stream=None):
+    """x [rows, cols] as E4M3 with one power-of-two scale for each block of block_rows x 128
+    values (block_rows 1: activations, 128: weights); cols % 8 == 0.  Returns (q, scales),
+    q float8_e4m3fn [rows, cols], scales fp32 [ceil(rows / block_rows), ceil(cols / 128)]."""
+    dt = _float_dtype(x, "x")
+    rows, cols = _require_matrix(x, x.dtype, "x")
+    if block_rows not in (1, BLOCK):
+        raise ValueError("block_rows must be 1 or 128")
+    out = _out(out, (rows, cols), FP8, "out", x.device, stream)
+    scales = _out(scales, (-(-rows // block_rows), _blocks(cols)), torch.float32, "scales", x.device, stream)
+    _check(_fn("fp8_block_quantize")(_p(x), dt, rows, cols, block_rows, _p(out), _p(scales), _stream(stream)),
+           "fp8_block_quantize")
+    return out, scales
+
+
+def fp8_block_dequantize(q: torch.Tensor, scales: torch.Tensor, block_rows: int = 1,
+                         out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                         stream=None) -> torch.Tensor:
+    """The values that (q, scales) of fp8_block_quantize stand for, in out_dtype."""
+    rows, cols = _require_matrix(q, FP8, "q")
+    if block_rows not in (1, BLOCK):
+        raise ValueError("block_rows must be 1 or 128")
+    if out_dtype not in TQ_DTYPE:
+        raise TypeError("out_dtype must be fp16, bf16 or fp32")
+    _require_dense(scales, torch.float32, (-(-rows // block_rows), _blocks(cols)), "scales")
+    out = _out(out, (rows, cols), out_dtype, "out", q.device, stream)
+    _check(_fn("fp8_block_dequantize")(_p(q), _p(scales), rows, cols, block_rows, _p(out), TQ_DTYPE[out_dtype],
+                                       _stream(stream)), "fp8_block_dequantize")
+    return out
+
+
+def _fp8_weight(w, s_w, K):
+    N, wk = _require_matrix(w, FP8, "w")
+    if wk != K:
+        raise ValueError("w has %d inputs, x has %d" % (wk, K))
+    _require_dense(s_w, torch.float32, (_blocks(N), _blocks(K)), "s_w")
+    return N
+
+
+def _fp8_out(out, out_dtype, shape, device, accumulate, stream):
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    if out_dtype is None:
+        out_dtype = out.dtype if isinstance(out, torch.Tensor) else torch.bfloat16
+    if out_dtype not in TQ_DTYPE:
+        raise TypeError("out_dtype must be fp16, bf16 or fp32")
+    return _out(out, shape, out_dtype, "out", device, stream)
+
+
+def fp8_block_gemm(x: torch.Tensor, s_x: torch.Tensor, w: torch.Tensor, s_w: torch.Tensor,
+                   out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                   accumulate: bool = False, stream=None) -> torch.Tensor:
+    """x [M, K] w [N, K]^T of E4M3 matrices with scales s_x [M, ceil(K/128)] and s_w
+    [ceil(N/128), ceil(K/128)]; K % 16 == 0.  out [M, N] in out_dtype (bf16 unless out or
+    out_dtype says otherwise); accumulate (fp32 out only) adds the product to out."""
+    M, K = _require_matrix(x, FP8, "x")
+    _require_dense(s_x, torch.float32, (M, _blocks(K)), "s_x")
+    N = _fp8_weight(w, s_w, K)
+    out = _fp8_out(out, out_dtype, (M, N), x.device, accumulate, stream)
+    _check(_fn("fp8_block_gemm")(_p(x), _p(s_x), _p(w), _p(s_w), M, N, K, _p(out), TQ_DTYPE[out.dtype],
+                                 int(accumulate), _stream(stream)), "fp8_block_gemm")
+    return out
+
+
+def fp8_block_linear_workspace_size(M: int, K: int) -> int:
+    return int(_fn("fp8_block_linear_workspace_size")(M, K))
+
+
+def fp8_block_linear(x: torch.Tensor, w: torch.Tensor, s_w: torch.Tensor, out: Optional[torch.Tensor] = None,
+                     out_dtype: Optional[torch.dtype] = None, accumulate: bool = False,
+                     ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """fp8_block_gemm of activations x [M, K] (fp16, bf16 or fp32), which are stored in
+    1 x 128 E4M3 blocks on the way (as fp8_block_quantize does)."""
+    dt = _float_dtype(x, "x")
+    M, K = _require_matrix(x, x.dtype, "x")
+    N = _fp8_weight(w, s_w, K)
+    out = _fp8_out(out, out_dtype, (M, N), x.device, accumulate, stream)
+    ws = _workspace(ws, fp8_block_linear_workspace_size(M, K), x.device, stream)
+    _check(_fn("fp8_block_linear")(_p(x), dt, _p(w), _p(s_w), M, N, K, _p(out), TQ_DTYPE[out.dtype], int(accumulate),
+                                   _p(ws), ws.numel() * ws.element_size(), _stream(stream)), "fp8_block_linear")
+    return out
+
+
+@dataclass
+class SwigluSaved:
+    """A SwiGLU block's activations in 8 bits (E4M3 and fp32 scales of 1 x 128 blocks): its
+    input x [T, D] and the projections before the activation g and u [T, F]."""
+    x: torch.Tensor
+    s_x: torch.Tensor
+    g: torch.Tensor
+    s_g: torch.Tensor
+    u: torch.Tensor
+    s_u: torch.Tensor
+
+    @staticmethod
+    def empty(T: int, D: int, F: int, device="cuda") -> "SwigluSaved":
+        def pair(n):
+            return (torch.empty((T, n), dtype=FP8, device=device),
+                    torch.empty((T, _blocks(n)), dtype=torch.float32, device=device))
+        return SwigluSaved(*pair(D), *pair(F), *pair(F))
+
+    def struct(self, T: int, D: int, F: int) -> TqSwigluSaved:
+        st = TqSwigluSaved()
+        for name, n in (("x", D), ("g", F), ("u", F)):
+            q, s = getattr(self, name), getattr(self, "s_" + name)
+            _require_dense(q, FP8, (T, n), "saved." + name)
+            _require_dense(s, torch.float32, (T, _blocks(n)), "saved.s_" + name)
+            setattr(st, name, q.data_ptr())
+            setattr(st, "s_" + name, s.data_ptr())
+        return st
+
+
+def _swiglu_weights(w_gate, w_up, dtype):
+    F, D = _require_matrix(w_gate, dtype, "w_gate")
+    _require_dense(w_up, dtype, (F, D), "w_up")
+    return F, D
+
+
+def swiglu_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, out: Optional[torch.Tensor] = None,
+                   saved: Optional[SwigluSaved] = None, stream=None) -> torch.Tensor:
+    """h = silu(x w_gate^T) * (x w_up^T): x [T, D], w_gate and w_up [F, D], all bf16 or all
+    fp16, D and F multiples of 8; h [T, F].  `saved` receives x and the two projections in
+    8 bits for swiglu_backward."""
+    dt = _float_dtype(x, "x")
+    T, D = _require_matrix(x, x.dtype, "x")
+    F, wd = _swiglu_weights(w_gate, w_up, x.dtype)
+    if wd != D:
+        raise ValueError("w_gate has %d inputs, x has %d" % (wd, D))
+    st = saved.struct(T, D, F) if saved is not None else None
+    out = _out(out, (T, F), x.dtype, "out", x.device, stream)
+    _check(_fn("swiglu_forward")(_p(x), _p(w_gate), _p(w_up), dt, T, D, F, _p(out),
+                                 ctypes.byref(st) if st is not None else None, _stream(stream)), "swiglu_forward")
+    return out
+
+
+def swiglu_backward_workspace_size(T: int, D: int, F: int, from_saved: bool) -> int:
+    return int(_fn("swiglu_backward_workspace_size")(T, D, F, int(from_saved)))
+
+
+def swiglu_backward(dh: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, x: Optional[torch.Tensor] = None,
+                    saved: Optional[SwigluSaved] = None, dx: Optional[torch.Tensor] = None,
+                    dw_gate: Optional[torch.Tensor] = None, dw_up: Optional[torch.Tensor] = None,
+                    ws: Optional[torch.Tensor] = None, stream=None):
+    """Gradients (dx [T, D], dw_gate [F, D], dw_up [F, D]) of swiglu_forward for dh [T, F], all
+    bf16, from exactly one of x (the projections are computed again) and saved."""
+    if (x is None) == (saved is None):
+        raise ValueError("swiglu_backward takes exactly one of x and saved")
+    dt = _float_dtype(dh, "dh")
+    T, hf = _require_matrix(dh, dh.dtype, "dh")
+    F, D = _swiglu_weights(w_gate, w_up, dh.dtype)
+    if hf != F:
+        raise ValueError("dh has %d columns, w_gate has %d outputs" % (hf, F))
+    if x is not None:
+        _require_dense(x, dh.dtype, (T, D), "x")
+    st = saved.struct(T, D, F) if saved is not None else None
+    dx = _out(dx, (T, D), dh.dtype, "dx", dh.device, stream)
+    dw_gate = _out(dw_gate, (F, D), dh.dtype, "dw_gate", dh.device, stream)
+    dw_up = _out(dw_up, (F, D), dh.dtype, "dw_up", dh.device, stream)
+    ws = _workspace(ws, swiglu_backward_workspace_size(T, D, F, saved is not None), dh.device, stream)
+    _check(_fn("swiglu_backward")(_p(dh), _p(x), ctypes.byref(st) if st is not None else None, _p(w_gate), _p(w_up),
+                                  dt, T, D, F, _p(dx), _p(dw_gate), _p(dw_up), _p(ws),
+                                  ws.numel() * ws.element_size(), _stream(stream)), "swiglu_backward")
+    return dx, dw_gate, dw_up
+
+
 class DeviceLayer:
     """A trellis-coded MoE layer resident on the GPU, with its C-ABI descriptor.
 
@@ -500,10 +743,39 @@ def moe_trellis_gemm(layer, x_rot, routing, T, k, y_perm=None, ws=None, stream=N
     return _moe_call("moe_trellis_gemm", layer, x_rot, routing, T, k, y_perm, ws, stream)
 
 
-class MoeBuffers:
-    """Preallocated device buffers of one MoE layer call (T tokens, top-k)."""
+@dataclass
+class SharedExpert:
+    """The dense expert of a layer, which every token uses: SwiGLU projections w_gate and w_up
+    [F, D] (bf16 or fp16, the type of the layer's input) and an FP8 down projection w_down
+    [D, F] (float8_e4m3fn) with s_down [ceil(D/128), ceil(F/128)]; F % 16 == 0."""
+    w_gate: torch.Tensor
+    w_up: torch.Tensor
+    w_down: torch.Tensor
+    s_down: torch.Tensor
 
-    def __init__(self, layer: DeviceLayer, T: int, k: int):
+    @staticmethod
+    def from_dense(w_gate: torch.Tensor, w_up: torch.Tensor, w_down: torch.Tensor, stream=None) -> "SharedExpert":
+        """From three dense matrices; w_down [D, F] is stored in 128 x 128 E4M3 blocks."""
+        return SharedExpert(w_gate, w_up, *fp8_block_quantize(w_down, BLOCK, stream=stream))
+
+    @property
+    def F(self) -> int:
+        return self.w_gate.shape[0]
+
+
+def shared_expert(shared: SharedExpert, x: torch.Tensor, out: Optional[torch.Tensor] = None, accumulate: bool = False,
+                  h: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """The dense expert's output [T, D] in fp32, or (accumulate) added to out: SwiGLU, then the
+    FP8 down projection.  h [T, F] and ws are optional buffers."""
+    h = swiglu_forward(x, shared.w_gate, shared.w_up, h, stream=stream)
+    return fp8_block_linear(h, shared.w_down, shared.s_down, out, torch.float32, accumulate, ws, stream)
+
+
+class MoeBuffers:
+    """Preallocated device buffers of one MoE layer call (T tokens, top-k; `shared`: the
+    dense expert the call adds, if any)."""
+
+    def __init__(self, layer: DeviceLayer, T: int, k: int, shared: Optional["SharedExpert"] = None):
         dev = layer.device
         self.T, self.k = T, k
         self.ids = torch.empty((T, k), dtype=torch.int32, device=dev)
@@ -514,18 +786,25 @@ class MoeBuffers:
         self.out = torch.empty((T, layer.D), dtype=torch.float32, device=dev)
         self.ws = torch.empty(max(moe_trellis_workspace_size(layer, T, k), 1), dtype=torch.uint8,
                               device=dev)
+        self.shared_h = self.shared_ws = None
+        if shared is not None:
+            self.shared_h = torch.empty((T, shared.F), dtype=shared.w_gate.dtype, device=dev)
+            self.shared_ws = torch.empty(max(fp8_block_linear_workspace_size(T, shared.F), 16), dtype=torch.uint8,
+                                         device=dev)
 
 
 GEMM_MIN_TOKENS = 340   # measured crossover of the two paths on the 384-expert decode layer
 
 
 def moe_layer(layer: DeviceLayer, x: torch.Tensor, logits: torch.Tensor, k: int,
-              bufs: Optional[MoeBuffers] = None, path: str = "auto", stream=None) -> torch.Tensor:
+              bufs: Optional[MoeBuffers] = None, path: str = "auto", stream=None,
+              shared: Optional[SharedExpert] = None) -> torch.Tensor:
     """One MoE layer's routed experts: top-k routing, grouping, input rotation, the
-    trellis GEMV (decode-sized T) or GEMM (prefill-sized T), and the combine.
+    trellis GEMV (decode-sized T) or GEMM (prefill-sized T), and the combine; with
+    `shared`, plus the dense expert's output.
     x: [T, D] bf16/fp16; logits: [T, E] fp32.  Returns out [T, D] fp32."""
     T = x.shape[0]
-    bufs = bufs or MoeBuffers(layer, T, k)
+    bufs = bufs or MoeBuffers(layer, T, k, shared)
     route_topk_permute(logits, k, layer.E, bufs.ids, bufs.w, bufs.routing, stream)
     if layer.signs is not None:
         hadamard128_signed(x, layer.signs["x"], bufs.x_rot, stream)
@@ -539,6 +818,8 @@ def moe_layer(layer: DeviceLayer, x: torch.Tensor, logits: torch.Tensor, k: int,
         route_unpermute_signed(bufs.y_perm, bufs.routing.inv, bufs.w, layer.signs["y"], bufs.out, stream)
     else:
         route_unpermute(bufs.y_perm, bufs.routing.inv, bufs.w, bufs.out, stream)
+    if shared is not None:
+        shared_expert(shared, x, bufs.out, True, bufs.shared_h, bufs.shared_ws, stream)
     return bufs.out
 
 
@@ -547,25 +828,27 @@ class MoeGraph:
 
     replay() copies x_host [T, D] (bf16/fp16) and logits_host [T, E] (fp32), both pinned,
     to the device, runs moe_layer (routing, rotation, expert path, combine) and copies the
-    result into out_host [T, D] fp32 (pinned), all as one graph launch on `stream`.  The
+    result into out_host [T, D] fp32 (pinned), all as one graph launch on `stream` (with
+    `shared`, the dense expert's output added).  The
     same host buffers are read and written on every replay: write the next step's inputs
     into x_host / logits_host, replay, read out_host after synchronising the stream.
     The first calls run eagerly (the library configures its kernels on first use, which
     must happen outside a capture)."""
 
     def __init__(self, layer: DeviceLayer, x_host: torch.Tensor, logits_host: torch.Tensor, k: int,
-                 path: str = "auto", out_host: Optional[torch.Tensor] = None, stream=None, warmup: int = 2):
+                 path: str = "auto", out_host: Optional[torch.Tensor] = None, stream=None, warmup: int = 2,
+                 shared: Optional[SharedExpert] = None):
         for t, name in ((x_host, "x_host"), (logits_host, "logits_host")):
             if t.is_cuda or not t.is_pinned():
                 raise ValueError("MoeGraph: %s must be pinned host memory" % name)
         T = x_host.shape[0]
-        self.layer, self.k, self.path = layer, k, path
+        self.layer, self.k, self.path, self.shared = layer, k, path, shared
         self.x_host, self.logits_host = x_host, logits_host
         self.out_host = out_host if out_host is not None else \
             torch.empty((T, layer.D), dtype=torch.float32).pin_memory()
         self.x = torch.empty(x_host.shape, dtype=x_host.dtype, device="cuda")
         self.logits = torch.empty(logits_host.shape, dtype=logits_host.dtype, device="cuda")
-        self.bufs = MoeBuffers(layer, T, k)
+        self.bufs = MoeBuffers(layer, T, k, shared)
         self.stream = stream if stream is not None else torch.cuda.Stream()
         self.stream.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(self.stream):
@@ -579,7 +862,8 @@ class MoeGraph:
     def _body(self):
         self.x.copy_(self.x_host, non_blocking=True)
         self.logits.copy_(self.logits_host, non_blocking=True)
-        out = moe_layer(self.layer, self.x, self.logits, self.k, bufs=self.bufs, path=self.path)
+        out = moe_layer(self.layer, self.x, self.logits, self.k, bufs=self.bufs, path=self.path,
+                        shared=self.shared)
         self.out_host.copy_(out, non_blocking=True)
 
     def replay(self) -> torch.Tensor:

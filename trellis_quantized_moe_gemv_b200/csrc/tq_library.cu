@@ -8,3 +8,5 @@
 #include "tq_gemm.cu"
 #include "tq_noalloc.cu"
 #include "tq_encode.cu"
+#include "tq_fp8.cu"
+#include "tq_swiglu.cu"

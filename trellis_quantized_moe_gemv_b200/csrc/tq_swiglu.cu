@@ -1,0 +1,560 @@
+// Gated feed-forward block (SwiGLU) of a dense expert and its gradient.
+//
+//   g = x Wg^T, u = x Wu^T, h = silu(g) * u
+//   dg = dh u s (1 + g (1 - s)), du = dh g s   (s = 1 / (1 + e^-g))
+//   dx = dg Wg + du Wu, dWg = dg^T x, dWu = du^T x
+//
+// Three products, all by one persistent CTA-pair kernel (tcgen05, cta_group::2): a pair
+// owns a 256 x 256 tile of fp32 accumulators, each CTA its 128 rows in its own tensor
+// memory (two tiles of 256 columns: the epilogue of one tile runs under the MMAs of the
+// next).  Per K-block of 64 each CTA brings in its half of both operands (2 x 16 KB, 6
+// stages) by TMA; the leader's MMA thread issues 4 MMAs of 256 x 256 x 16.
+//   * gate/up: the B operand's first half is 128 gate rows (CTA 0), its second half the
+//     same 128 up rows (CTA 1), so a row's g and u meet in one thread's epilogue, which
+//     writes h, or (backward) reads dh and writes dg and du.  128 columns are also one
+//     scale block: the thread that holds a row of it stores g and u in 8 bits.
+//   * gradients: one launch takes the tiles of dWg and dWu (both operands MN-major: K runs
+//     over the tokens) and then those of dx (A K-major, B MN-major; K runs over Wg's rows
+//     and then Wu's), so the long weight-gradient tiles start first and the dx tiles fill
+//     the pairs that finish early.
+// dg and du are rounded to bf16 between the two launches: the tensor cores take 16-bit
+// operands, and a rounding of 2^-9 in independent terms of a sum changes the sum by less
+// than the rounding of the 16-bit gradient itself.
+//
+// Few tokens: dense_rows_kernel (weights streamed once, tokens on the MMA's N side).
+#include "tq_dense_rows.cuh"
+
+namespace tq {
+
+constexpr int kPairM = 256, kPairN = 256;
+constexpr int kPairStages = 6;
+constexpr int kPairThreads = 384;      // warp 0 TMA, 1 MMA (leader), 2 TMEM, 4-11 epilogue
+constexpr int kPairStageBytes = 16384;
+
+struct __align__(1024) PairSmem {
+    unsigned char a[kPairStages][kPairStageBytes];
+    unsigned char b[kPairStages][kPairStageBytes];
+    uint64_t full[kPairStages];     // leader: both CTAs' copies of the stage
+    uint64_t empty[kPairStages];    // MMA commit, in both CTAs
+    uint64_t acc_full[2];           // MMA commit, in both CTAs
+    uint64_t acc_empty[2];          // leader: the 16 epilogue warps of the pair
+    uint32_t tmem_base;
+    int32_t abort;
+};
+static_assert(sizeof(PairSmem) + 1024 <= 227 * 1024, "pair GEMM shared memory");
+
+// gate/up: a0 = x, b0 = Wg, b1 = Wu.  Gradients: a0 = dg, a1 = du, b0 = Wg, b1 = Wu, x = x.
+// Every map reads boxes of 64 x 64 elements.
+struct PairMaps {
+    CUtensorMap a0, a1, b0, b1, x;
+};
+
+struct PairArgs {
+    int T, D, F;
+    int f16;                                  // 16-bit type: 1 fp16, 0 bf16
+    void *h;                                  // [T][F]
+    uint8_t *g8, *u8;                         // [T][F] E4M3, or null
+    float *sg, *su;                           // [T][ceil(F / 128)]
+    const __nv_bfloat16 *dh;                  // [T][F]
+    __nv_bfloat16 *dg, *du;                   // [T][F]
+    __nv_bfloat16 *dx, *dwg, *dwu;            // [T][D], [F][D], [F][D]
+};
+
+enum PairKind { kPairForward = 0, kPairSave = 1, kPairRecompute = 2, kPairGrads = 3 };
+
+// One output tile: rows m0 .. m0 + 255 of the pair, columns n0 .. n0 + 255 (gate/up: 128
+// outputs), `which` the matrix of a weight gradient (0 gate, 1 up; -1 dx).
+struct PairTile {
+    int m0, n0, kblocks, which;
+};
+
+template <int KIND>
+__device__ __forceinline__ long long pair_tiles(const PairArgs &p) {
+    const long long mt = (p.T + kPairM - 1) / kPairM;
+    if (KIND != kPairGrads) return mt * ((p.F + 127) / 128);
+    const long long nd = (p.D + kPairN - 1) / kPairN;
+    return (2LL * ((p.F + kPairM - 1) / kPairM) + mt) * nd;
+}
+
+template <int KIND>
+__device__ __forceinline__ PairTile pair_tile(const PairArgs &p, long long t) {
+    PairTile r;
+    int m, n;
+    if (KIND != kPairGrads) {
+        grouped_tile(t, (p.T + kPairM - 1) / kPairM, (p.F + 127) / 128, m, n);
+        r.m0 = m * kPairM;
+        r.n0 = n * 128;
+        r.kblocks = (p.D + 63) / 64;
+        r.which = -1;
+        return r;
+    }
+    const int nd = (p.D + kPairN - 1) / kPairN, mf = (p.F + kPairM - 1) / kPairM;
+    const long long dw = 2LL * mf * nd;
+    if (t < dw) {
+        grouped_tile(t, 2 * mf, nd, m, n);
+        r.which = m >= mf;
+        r.m0 = (m - (r.which ? mf : 0)) * kPairM;
+        r.kblocks = (p.T + 63) / 64;
+    } else {
+        grouped_tile(t - dw, (p.T + kPairM - 1) / kPairM, nd, m, n);
+        r.which = -1;
+        r.m0 = m * kPairM;
+        r.kblocks = 2 * ((p.F + 63) / 64);
+    }
+    r.n0 = n * kPairN;
+    return r;
+}
+
+// ------------------------------------------------------------------------------ epilogues
+
+__device__ __forceinline__ void store_row16(void *base, size_t i, const float *v, int n, bool f16) {
+    uint4 *p = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(base) + i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (8 * j < n)
+            p[j] = make_uint4(pack16(v[8 * j], v[8 * j + 1], f16), pack16(v[8 * j + 2], v[8 * j + 3], f16),
+                              pack16(v[8 * j + 4], v[8 * j + 5], f16), pack16(v[8 * j + 6], v[8 * j + 7], f16));
+}
+
+// One warp's share of a tile: tensor-memory lane quarter q (rows), column half w.
+template <int KIND>
+__device__ __forceinline__ void pair_epilogue(const PairArgs &p, const PairTile &t, uint32_t taddr, int row, int w) {
+    uint32_t a[32], b[32];
+    float v[32];
+    if constexpr (KIND == kPairGrads) {
+        __nv_bfloat16 *out = t.which < 0 ? p.dx : (t.which ? p.dwu : p.dwg);
+        const int rows = t.which < 0 ? p.T : p.F;
+        const int r = t.m0 + row;
+#pragma unroll 1
+        for (int c = 128 * w; c < 128 * w + 128; c += 32) {
+            tmem_ld32(taddr + c, a);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(a[i]);
+            const int col = t.n0 + c;
+            if (r < rows) store_row16(out, (size_t)r * p.D + col, v, p.D - col, false);
+        }
+        return;
+    }
+    const int r = t.m0 + row;
+    if constexpr (KIND == kPairSave) {
+        // column half w stores matrix w (0: g, 1: u) of the 128-wide block in 8 bits
+        const uint32_t m_addr = taddr + 128 * w;
+        float m = 0.f;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+            tmem_ld32(m_addr + c, a);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) m = finite_max(m, __uint_as_float(a[i]));   // columns past F hold zeros
+        }
+        const int e = e4m3_block_exponent(m);
+        const float inv = exp2_int(-e);
+        const int fb = (p.F + 127) / 128;
+        if (r < p.T) (w ? p.su : p.sg)[(size_t)r * fb + t.n0 / 128] = exp2_int(e);
+        uint8_t *q = (w ? p.u8 : p.g8) + (size_t)r * p.F + t.n0;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+            tmem_ld32(m_addr + c, a);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+                const uint32_t lo = e4m3x4_scaled(__uint_as_float(a[i]), __uint_as_float(a[i + 1]),
+                                                  __uint_as_float(a[i + 2]), __uint_as_float(a[i + 3]), inv);
+                const uint32_t hi = e4m3x4_scaled(__uint_as_float(a[i + 4]), __uint_as_float(a[i + 5]),
+                                                  __uint_as_float(a[i + 6]), __uint_as_float(a[i + 7]), inv);
+                if (r < p.T && t.n0 + c + i < p.F) *reinterpret_cast<uint2 *>(q + c + i) = make_uint2(lo, hi);
+            }
+        }
+    }
+#pragma unroll 1
+    for (int c = 64 * w; c < 64 * w + 64; c += 32) {
+        tmem_ld32(taddr + c, a);
+        tmem_ld32(taddr + 128 + c, b);
+        const int col = t.n0 + c;
+        if constexpr (KIND == kPairRecompute) {
+            uint4 d[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                d[j] = r < p.T && col + 8 * j < p.F
+                           ? __ldg(reinterpret_cast<const uint4 *>(p.dh + (size_t)r * p.F + col + 8 * j))
+                           : make_uint4(0, 0, 0, 0);
+            tmem_ld_wait();
+            float du[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const uint32_t w2 = reinterpret_cast<const uint32_t *>(d)[i >> 1];
+                const float dh = __uint_as_float((i & 1) ? (w2 & 0xFFFF0000u) : (w2 << 16));
+                swiglu_grads(__uint_as_float(a[i]), __uint_as_float(b[i]), dh, v[i], du[i]);
+            }
+            if (r < p.T) {
+                store_row16(p.dg, (size_t)r * p.F + col, v, p.F - col, false);
+                store_row16(p.du, (size_t)r * p.F + col, du, p.F - col, false);
+            }
+        } else {
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = swiglu_value(__uint_as_float(a[i]), __uint_as_float(b[i]));
+            if (r < p.T) store_row16(p.h, (size_t)r * p.F + col, v, p.F - col, p.f16 != 0);
+        }
+    }
+}
+
+// ------------------------------------------------------------------------------ kernel
+
+template <int KIND>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    pair_gemm_kernel(const __grid_constant__ PairMaps maps, const PairArgs args) {
+    extern __shared__ __align__(128) unsigned char smem_raw[];
+    const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
+    PairSmem &sm = *reinterpret_cast<PairSmem *>(smem_raw + pad);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();
+    const long long tiles = pair_tiles<KIND>(args);
+    const long long pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kPairStages; ++i) {
+            mbar_init(&sm.full[i], 1);
+            mbar_init(&sm.empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.acc_full[i], 1);
+            mbar_init(&sm.acc_empty[i], 16);
+        }
+        sm.abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == 2) tmem_alloc_pair(&sm.tmem_base, 512);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    chain_entry();
+
+    auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        if (*(volatile int32_t *)&sm.abort) return false;
+        const bool ok = mbar_wait_sleep(bar, parity);
+        if (!ok) sm.abort = 1;
+        return ok;
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            bool ok = true;
+            uint32_t it = 0;
+            // operand tile of 128 rows x 64 K in two 64 x 64 boxes: K-major (rows then K)
+            // or MN-major (K rows of 64 consecutive matrix columns)
+            auto load = [&](unsigned char *dst, const CUtensorMap *m, int r0, int k0, bool mn, uint32_t bar) {
+                tma_load_2d_pair(dst, m, mn ? r0 : k0, mn ? k0 : r0, bar);
+                tma_load_2d_pair(dst + 8192, m, mn ? r0 + 64 : k0, mn ? k0 : r0 + 64, bar);
+            };
+            for (long long t = pair; t < tiles && ok; t += pairs) {
+                const PairTile tl = pair_tile<KIND>(args, t);
+                const int half = (args.F + 63) / 64;      // dx: K-blocks of dg, then of du
+                for (int kb = 0; kb < tl.kblocks; ++kb, ++it) {
+                    const int s = it % kPairStages;
+                    if (it >= kPairStages && !wait(&sm.empty[s], (it / kPairStages - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t bar = map_to_rank(smem_u32(&sm.full[s]), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 4 * kPairStageBytes);
+                    const int ar = tl.m0 + 128 * rank;
+                    if (KIND != kPairGrads) {
+                        load(sm.a[s], &maps.a0, ar, kb * 64, false, bar);
+                        load(sm.b[s], rank ? &maps.b1 : &maps.b0, tl.n0, kb * 64, false, bar);
+                    } else if (tl.which >= 0) {
+                        load(sm.a[s], tl.which ? &maps.a1 : &maps.a0, ar, kb * 64, true, bar);
+                        load(sm.b[s], &maps.x, tl.n0 + 128 * rank, kb * 64, true, bar);
+                    } else {
+                        const bool up = kb >= half;
+                        const int k0 = (up ? kb - half : kb) * 64;
+                        load(sm.a[s], up ? &maps.a1 : &maps.a0, ar, k0, false, bar);
+                        load(sm.b[s], up ? &maps.b1 : &maps.b0, tl.n0 + 128 * rank, k0, true, bar);
+                    }
+                }
+            }
+            // every stage read by its MMAs before the CTA can exit; after a wait that gave
+            // up, time for the copies in flight to land
+            for (uint32_t i = it > kPairStages ? it - kPairStages : 0; i < it && ok; ++i)
+                ok = wait(&sm.empty[i % kPairStages], (i / kPairStages) & 1);
+            if (!ok)
+                for (int i = 0; i < 2000; ++i) __nanosleep(1000);
+        }
+    } else if (warp == 1) {
+        if (rank == 0 && lane == 0) {
+            bool ok = true;
+            uint32_t it = 0, j = 0;
+            const int fmt = args.f16 ? 0 : 1;
+            for (long long t = pair; t < tiles && ok; t += pairs, ++j) {
+                const PairTile tl = pair_tile<KIND>(args, t);
+                const bool a_mn = KIND == kPairGrads && tl.which >= 0, b_mn = KIND == kPairGrads;
+                const uint32_t idesc = umma_idesc(kPairM, kPairN, fmt, a_mn, b_mn);
+                const uint32_t st = j & 1, d = tmem + st * kPairN;
+                if (j >= 2 && !wait(&sm.acc_empty[st], ((j >> 1) - 1) & 1)) break;
+                tc_fence_after();
+                for (int kb = 0; kb < tl.kblocks; ++kb, ++it) {
+                    const int s = it % kPairStages;
+                    if (!wait(&sm.full[s], (it / kPairStages) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t as = smem_u32(sm.a[s]), bs = smem_u32(sm.b[s]);
+                    const uint64_t ad = a_mn ? umma_desc_mn_sw128(as) : umma_desc_sw128(as);
+                    const uint64_t bd = b_mn ? umma_desc_mn_sw128(bs) : umma_desc_sw128(bs);
+                    const uint32_t a_step = a_mn ? 128 : 2, b_step = b_mn ? 128 : 2;   // 16-byte units per K = 16
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_f16_pair(d, ad + k * a_step, bd + k * b_step, idesc, (kb | k) != 0);
+                    umma_commit_pair(&sm.empty[s]);
+                }
+                if (ok) umma_commit_pair(&sm.acc_full[st]);
+            }
+        }
+    } else if (warp >= 4) {
+        const int q = warp & 3, w = (warp - 4) >> 2;
+        const int row = 128 * rank + 32 * q + lane;
+        uint32_t j = 0;
+        for (long long t = pair; t < tiles; t += pairs, ++j) {
+            const PairTile tl = pair_tile<KIND>(args, t);
+            const uint32_t st = j & 1;
+            const bool ok = __all_sync(0xffffffffu, wait(&sm.acc_full[st], (j >> 1) & 1));
+            if (!ok) break;
+            tc_fence_after();
+            pair_epilogue<KIND>(args, tl, tmem + st * kPairN + ((uint32_t)(32 * q) << 16), row, w);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&sm.acc_empty[st]), 0));
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+// dg and du from the 8-bit g and u: 8 values a thread, one read of g8, u8 and dh and one
+// write of dg and du.  Memory-bound.
+__global__ void __launch_bounds__(256) swiglu_grads_saved_kernel(const uint8_t *__restrict__ g8,
+                                                                 const float *__restrict__ sg,
+                                                                 const uint8_t *__restrict__ u8,
+                                                                 const float *__restrict__ su,
+                                                                 const __nv_bfloat16 *__restrict__ dh, int T, int F,
+                                                                 __nv_bfloat16 *__restrict__ dg,
+                                                                 __nv_bfloat16 *__restrict__ du) {
+    chain_entry();
+    const int per_row = F / 8, fb = (F + 127) / 128;
+    const long long n = (long long)T * per_row;
+    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < n; i += gridDim.x * 256LL) {
+        const long long t = i / per_row;
+        const int f = (int)(i - t * per_row) * 8;
+        const size_t at = (size_t)t * F + f, sat = (size_t)t * fb + f / 128;
+        const uint2 gq = *reinterpret_cast<const uint2 *>(g8 + at), uq = *reinterpret_cast<const uint2 *>(u8 + at);
+        const uint4 d4 = *reinterpret_cast<const uint4 *>(dh + at);
+        const float gs = sg[sat], us = su[sat];
+        float g[8], u[8], a[8], b[8];
+        e4m3x4_to_f32(gq.x, *reinterpret_cast<float(*)[4]>(g));
+        e4m3x4_to_f32(gq.y, *reinterpret_cast<float(*)[4]>(g + 4));
+        e4m3x4_to_f32(uq.x, *reinterpret_cast<float(*)[4]>(u));
+        e4m3x4_to_f32(uq.y, *reinterpret_cast<float(*)[4]>(u + 4));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t w2 = reinterpret_cast<const uint32_t *>(&d4)[j >> 1];
+            const float d = __uint_as_float((j & 1) ? (w2 & 0xFFFF0000u) : (w2 << 16));
+            swiglu_grads(g[j] * gs, u[j] * us, d, a[j], b[j]);
+        }
+        *reinterpret_cast<uint4 *>(dg + at) =
+            make_uint4(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(a[4], a[5]), pack_bf16(a[6], a[7]));
+        *reinterpret_cast<uint4 *>(du + at) =
+            make_uint4(pack_bf16(b[0], b[1]), pack_bf16(b[2], b[3]), pack_bf16(b[4], b[5]), pack_bf16(b[6], b[7]));
+    }
+}
+
+// ------------------------------------------------------------------------------ host side
+
+static int pair_map(CUtensorMap *m, const void *base, long long rows, long long cols, int f16) {
+    return matrix_map(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, rows, cols,
+                      64);
+}
+
+template <int KIND>
+static int launch_pair(const PairMaps &maps, const PairArgs &p, cudaStream_t s, int stage) {
+    static PerDeviceFlag configured;
+    const int smem = (int)sizeof(PairSmem) + 1024;
+    if (!configured.get()) {
+        if (cudaFuncSetAttribute(pair_gemm_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+            cudaSuccess)
+            return record_cuda_error("cudaFuncSetAttribute(pair_gemm_kernel)");
+        configured.set();
+    }
+    const long long mt = ((long long)p.T + kPairM - 1) / kPairM;
+    long long tiles = mt * ((p.F + 127LL) / 128);
+    if (KIND == kPairGrads)
+        tiles = (2 * (((long long)p.F + kPairM - 1) / kPairM) + mt) * (((long long)p.D + kPairN - 1) / kPairN);
+    const long long pairs = num_sms() / 2;
+    const unsigned grid = 2 * (unsigned)(tiles < pairs ? tiles : pairs);
+    LaunchScope ls(s, stage);
+    if (launch_chained(pair_gemm_kernel<KIND>, dim3(grid), dim3(kPairThreads), smem, s, maps, p) != cudaSuccess)
+        return record_cuda_error("pair_gemm_kernel");
+    return launch_status();
+}
+
+static inline size_t align256_d(size_t n) { return (n + 255) & ~(size_t)255; }
+
+static int swiglu_shape_status(int T, int D, int F) {
+    if (T < 0 || D < 1 || F < 1 || D % 8 || F % 8) return TQ_ERR_INVALID_ARG;
+    return TQ_OK;
+}
+
+static bool saved_complete(const tq_swiglu_saved *s) { return s->x && s->s_x && s->g && s->s_g && s->u && s->s_u; }
+static bool saved_aligned(const tq_swiglu_saved *s) {
+    return aligned16(s->x) && aligned16(s->s_x) && aligned16(s->g) && aligned16(s->s_g) && aligned16(s->u) &&
+           aligned16(s->s_u);
+}
+
+// Up to this many tokens the weight-streaming kernel runs (tokens on the MMA's N side).
+constexpr int kSwigluRowsMost = 128;
+
+static int swiglu_rows(const void *x, const void *wg, const void *wu, int f16, int T, int D, int F, void *h,
+                       cudaStream_t s) {
+    const CUtensorMapDataType ty = f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const int n = T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
+    CUtensorMap mg, mu, mx;
+    int st = matrix_map(&mg, ty, 2, wg, F, D, 64);
+    if (!st) st = matrix_map(&mu, ty, 2, wu, F, D, 64);
+    if (!st) st = matrix_map(&mx, ty, 2, x, T, D, n);
+    if (st) return st;
+    RowsArgs a{};
+    a.rows = T;
+    a.width = F;
+    a.kblocks = (D + 63) / 64;
+    a.out_type = f16 ? TQ_DTYPE_F16 : TQ_DTYPE_BF16;
+    a.out = h;
+    LaunchScope ls(s, kStageSwiglu);
+    switch (n) {
+        case 16: return launch_rows<16, kSwiglu>(mg, mu, mx, a, s, true);
+        case 32: return launch_rows<32, kSwiglu>(mg, mu, mx, a, s, true);
+        case 64: return launch_rows<64, kSwiglu>(mg, mu, mx, a, s, true);
+        default: return launch_rows<128, kSwiglu>(mg, mu, mx, a, s, true);
+    }
+}
+
+}  // namespace tq
+
+TQ_API int swiglu_forward(const void *x, const void *w_gate, const void *w_up, int dtype, int T, int D, int F, void *h,
+                          const tq_swiglu_saved *saved, tq_stream stream) {
+    using namespace tq;
+    if (dtype != TQ_DTYPE_F16 && dtype != TQ_DTYPE_BF16)
+        return dtype == TQ_DTYPE_F32 ? TQ_ERR_UNSUPPORTED : TQ_ERR_INVALID_ARG;
+    int st = swiglu_shape_status(T, D, F);
+    if (st) return st;
+    if (T == 0) return TQ_OK;
+    if (!x || !w_gate || !w_up || !h || (saved && !saved_complete(saved))) return TQ_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(w_gate) || !aligned16(w_up) || !aligned16(h) || (saved && !saved_aligned(saved)))
+        return TQ_ERR_ALIGNMENT;
+    const cudaStream_t s = (cudaStream_t)stream;
+    const int f16 = dtype == TQ_DTYPE_F16;
+    if (!saved && T <= kSwigluRowsMost) return swiglu_rows(x, w_gate, w_up, f16, T, D, F, h, s);
+    if (saved) {
+        st = fp8_block_quantize(x, dtype, T, D, 1, saved->x, saved->s_x, stream);
+        if (st) return st;
+    }
+    PairMaps maps;
+    memset(&maps, 0, sizeof(maps));
+    st = pair_map(&maps.a0, x, T, D, f16);
+    if (!st) st = pair_map(&maps.b0, w_gate, F, D, f16);
+    if (!st) st = pair_map(&maps.b1, w_up, F, D, f16);
+    if (st) return st;
+    PairArgs p{};
+    p.T = T;
+    p.D = D;
+    p.F = F;
+    p.f16 = f16;
+    p.h = h;
+    if (!saved) return launch_pair<kPairForward>(maps, p, s, kStageSwiglu);
+    p.g8 = saved->g;
+    p.u8 = saved->u;
+    p.sg = saved->s_g;
+    p.su = saved->s_u;
+    return launch_pair<kPairSave>(maps, p, s, kStageSwiglu);
+}
+
+TQ_API size_t swiglu_backward_workspace_size(int T, int D, int F, int from_saved) {
+    if (tq::swiglu_shape_status(T, D, F)) return 0;
+    return 2 * tq::align256_d((size_t)T * F * 2) + (from_saved ? tq::align256_d((size_t)T * D * 2) : 0);
+}
+
+TQ_API int swiglu_backward(const void *dh, const void *x, const tq_swiglu_saved *saved, const void *w_gate,
+                           const void *w_up, int dtype, int T, int D, int F, void *dx, void *dw_gate, void *dw_up,
+                           void *ws, size_t ws_bytes, tq_stream stream) {
+    using namespace tq;
+    if (dtype != TQ_DTYPE_BF16)
+        return dtype == TQ_DTYPE_F16 || dtype == TQ_DTYPE_F32 ? TQ_ERR_UNSUPPORTED : TQ_ERR_INVALID_ARG;
+    int st = swiglu_shape_status(T, D, F);
+    if (st) return st;
+    if (!dw_gate || !dw_up) return TQ_ERR_INVALID_ARG;
+    if (!aligned16(dw_gate) || !aligned16(dw_up)) return TQ_ERR_ALIGNMENT;
+    const cudaStream_t s = (cudaStream_t)stream;
+    if (T == 0) {      // an empty batch: dx has no rows, the weight gradients are zero
+        if (cudaMemsetAsync(dw_gate, 0, (size_t)F * D * 2, s) != cudaSuccess ||
+            cudaMemsetAsync(dw_up, 0, (size_t)F * D * 2, s) != cudaSuccess)
+            return record_cuda_error("swiglu_backward: memset");
+        return TQ_OK;
+    }
+    if (!dh || !w_gate || !w_up || !dx || (x != nullptr) == (saved != nullptr)) return TQ_ERR_INVALID_ARG;
+    if (saved && !saved_complete(saved)) return TQ_ERR_INVALID_ARG;
+    if (!aligned16(dh) || !aligned16(w_gate) || !aligned16(w_up) || !aligned16(dx) || (x && !aligned16(x)) ||
+        (saved && !saved_aligned(saved)) || (ws && !aligned16(ws)))
+        return TQ_ERR_ALIGNMENT;
+    if (!ws || ws_bytes < swiglu_backward_workspace_size(T, D, F, saved != nullptr)) return TQ_ERR_WORKSPACE;
+
+    char *w = reinterpret_cast<char *>(ws);
+    PairArgs p{};
+    p.T = T;
+    p.D = D;
+    p.F = F;
+    p.dh = reinterpret_cast<const __nv_bfloat16 *>(dh);
+    p.dg = reinterpret_cast<__nv_bfloat16 *>(w);
+    w += align256_d((size_t)T * F * 2);
+    p.du = reinterpret_cast<__nv_bfloat16 *>(w);
+    w += align256_d((size_t)T * F * 2);
+    p.dx = reinterpret_cast<__nv_bfloat16 *>(dx);
+    p.dwg = reinterpret_cast<__nv_bfloat16 *>(dw_gate);
+    p.dwu = reinterpret_cast<__nv_bfloat16 *>(dw_up);
+    PairMaps maps;
+    memset(&maps, 0, sizeof(maps));
+    st = pair_map(&maps.b0, w_gate, F, D, 0);
+    if (!st) st = pair_map(&maps.b1, w_up, F, D, 0);
+    if (st) return st;
+    const void *xb = x;
+    if (saved) {
+        // x as bf16: exact, an E4M3 value times a power of two (down to bf16's least subnormal)
+        st = fp8_block_dequantize(saved->x, saved->s_x, T, D, 1, w, TQ_DTYPE_BF16, stream);
+        if (st) return st;
+        xb = w;
+        const long long n = (long long)T * (F / 8);
+        const long long blocks = (n + 255) / 256, most = 8LL * num_sms();
+        LaunchScope ls(s, kStageSwigluGrad);
+        if (launch_chained(swiglu_grads_saved_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, s,
+                           (const uint8_t *)saved->g, (const float *)saved->s_g, (const uint8_t *)saved->u,
+                           (const float *)saved->s_u, p.dh, T, F, p.dg, p.du) != cudaSuccess)
+            return record_cuda_error("swiglu_grads_saved_kernel");
+    } else {
+        st = pair_map(&maps.a0, x, T, D, 0);
+        if (st) return st;
+        st = launch_pair<kPairRecompute>(maps, p, s, kStageSwigluGrad);
+    }
+    if (st) return st;
+    st = pair_map(&maps.a0, p.dg, T, F, 0);
+    if (!st) st = pair_map(&maps.a1, p.du, T, F, 0);
+    if (!st) st = pair_map(&maps.x, xb, T, D, 0);
+    if (st) return st;
+    return launch_pair<kPairGrads>(maps, p, s, kStageSwigluGrad);
+}
