@@ -409,50 +409,61 @@ def _blocks(n: int) -> int:
     return -(-n // BLOCK)
 
 
-def _require_dense(t, dtype, shape, name):
-    """A contiguous CUDA tensor of this dtype (None: any the entry point takes) and shape, on
-    the current device, where the kernels run."""
-    _require(t, t.dtype if dtype is None and isinstance(t, torch.Tensor) else dtype, name)
-    if tuple(t.shape) != tuple(shape):
+def _require_dense(t, dtype, shape, name, dev):
+    """A contiguous CUDA tensor of this dtype and shape on the current device `dev`, where the
+    kernels run.  One expression decides the usual case: these checks are a good part of a
+    call that takes a few microseconds."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.get_device() == dev
+            and t.shape == shape and t.is_contiguous()):
+        return
+    _require(t, dtype, name)
+    if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError("%s is on %s, but the current device is cuda:%d" % (name, t.device, torch.cuda.current_device()))
+    raise ValueError("%s is on %s, but the current device is cuda:%d" % (name, t.device, dev))
 
 
 def _require_matrix(t, dtype, name):
+    """(rows, columns, current device) of a contiguous matrix on the current device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.dim() != 2:
         raise ValueError("%s must be a matrix, got %d dimensions" % (name, t.dim()))
-    _require_dense(t, dtype, t.shape, name)
-    return t.shape
+    if not t.is_cuda:
+        _require(t, dtype, name)
+    dev = torch.cuda.current_device()
+    _require_dense(t, dtype, t.shape, name, dev)
+    return t.shape[0], t.shape[1], dev
 
 
-def _new(shape, dtype, device, stream):
+def _raw_stream(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+def _new(shape, dtype, dev, stream):
     """An uninitialised tensor for a call on `stream` (None: the current stream).  Memory for
     another stream comes from that stream's pool, so that nothing still running on the
     current stream owns it, and is kept until the current stream's uses of it are over."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=device)
+        t = torch.empty(shape, dtype=dtype, device=dev)
     t.record_stream(torch.cuda.current_stream())
     return t
 
 
-def _out(out, shape, dtype, name, device, stream):
+def _out(out, shape, dtype, name, dev, stream):
     if out is None:
-        return _new(shape, dtype, device, stream)
-    _require_dense(out, dtype, shape, name)
+        return _new(shape, dtype, dev, stream)
+    _require_dense(out, dtype, shape, name, dev)
     return out
 
 
-def _workspace(ws, need, device, stream):
+def _workspace(ws, need, dev, stream):
     if ws is None:
-        return _new(max(need, 16), torch.uint8, device, stream)
+        return _new(max(need, 16), torch.uint8, dev, stream)
     if not isinstance(ws, torch.Tensor):
         raise TypeError("ws must be a torch.Tensor")
-    _require_dense(ws, None, ws.shape, "ws")
+    _require_dense(ws, ws.dtype, ws.shape, "ws", dev)
     return ws
 
 
@@ -468,13 +479,13 @@ def fp8_block_quantize(x: torch.Tensor, block_rows: int = 1, out: Optional[torch
     values (block_rows 1: activations, 128: weights); cols % 8 == 0.  Returns (q, scales),
     q float8_e4m3fn [rows, cols], scales fp32 [ceil(rows / block_rows), ceil(cols / 128)]."""
     dt = _float_dtype(x, "x")
-    rows, cols = _require_matrix(x, x.dtype, "x")
+    rows, cols, dev = _require_matrix(x, x.dtype, "x")
     if block_rows not in (1, BLOCK):
         raise ValueError("block_rows must be 1 or 128")
-    out = _out(out, (rows, cols), FP8, "out", x.device, stream)
-    scales = _out(scales, (-(-rows // block_rows), _blocks(cols)), torch.float32, "scales", x.device, stream)
-    _check(_fn("fp8_block_quantize")(_p(x), dt, rows, cols, block_rows, _p(out), _p(scales), _stream(stream)),
-           "fp8_block_quantize")
+    out = _out(out, (rows, cols), FP8, "out", dev, stream)
+    scales = _out(scales, (-(-rows // block_rows), _blocks(cols)), torch.float32, "scales", dev, stream)
+    _check(_fn("fp8_block_quantize")(x.data_ptr(), dt, rows, cols, block_rows, out.data_ptr(), scales.data_ptr(),
+                                     _raw_stream(stream, dev)), "fp8_block_quantize")
     return out, scales
 
 
@@ -482,34 +493,34 @@ def fp8_block_dequantize(q: torch.Tensor, scales: torch.Tensor, block_rows: int 
                          out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
                          stream=None) -> torch.Tensor:
     """The values that (q, scales) of fp8_block_quantize stand for, in out_dtype."""
-    rows, cols = _require_matrix(q, FP8, "q")
+    rows, cols, dev = _require_matrix(q, FP8, "q")
     if block_rows not in (1, BLOCK):
         raise ValueError("block_rows must be 1 or 128")
     if out_dtype not in TQ_DTYPE:
         raise TypeError("out_dtype must be fp16, bf16 or fp32")
-    _require_dense(scales, torch.float32, (-(-rows // block_rows), _blocks(cols)), "scales")
-    out = _out(out, (rows, cols), out_dtype, "out", q.device, stream)
-    _check(_fn("fp8_block_dequantize")(_p(q), _p(scales), rows, cols, block_rows, _p(out), TQ_DTYPE[out_dtype],
-                                       _stream(stream)), "fp8_block_dequantize")
+    _require_dense(scales, torch.float32, (-(-rows // block_rows), _blocks(cols)), "scales", dev)
+    out = _out(out, (rows, cols), out_dtype, "out", dev, stream)
+    _check(_fn("fp8_block_dequantize")(q.data_ptr(), scales.data_ptr(), rows, cols, block_rows, out.data_ptr(),
+                                       TQ_DTYPE[out_dtype], _raw_stream(stream, dev)), "fp8_block_dequantize")
     return out
 
 
-def _fp8_weight(w, s_w, K):
-    N, wk = _require_matrix(w, FP8, "w")
+def _fp8_weight(w, s_w, K, dev):
+    N, wk, _ = _require_matrix(w, FP8, "w")
     if wk != K:
         raise ValueError("w has %d inputs, x has %d" % (wk, K))
-    _require_dense(s_w, torch.float32, (_blocks(N), _blocks(K)), "s_w")
+    _require_dense(s_w, torch.float32, (_blocks(N), _blocks(K)), "s_w", dev)
     return N
 
 
-def _fp8_out(out, out_dtype, shape, device, accumulate, stream):
+def _fp8_out(out, out_dtype, shape, dev, accumulate, stream):
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     if out_dtype is None:
         out_dtype = out.dtype if isinstance(out, torch.Tensor) else torch.bfloat16
     if out_dtype not in TQ_DTYPE:
         raise TypeError("out_dtype must be fp16, bf16 or fp32")
-    return _out(out, shape, out_dtype, "out", device, stream)
+    return _out(out, shape, out_dtype, "out", dev, stream)
 
 
 def fp8_block_gemm(x: torch.Tensor, s_x: torch.Tensor, w: torch.Tensor, s_w: torch.Tensor,
@@ -518,12 +529,12 @@ def fp8_block_gemm(x: torch.Tensor, s_x: torch.Tensor, w: torch.Tensor, s_w: tor
     """x [M, K] w [N, K]^T of E4M3 matrices with scales s_x [M, ceil(K/128)] and s_w
     [ceil(N/128), ceil(K/128)]; K % 16 == 0.  out [M, N] in out_dtype (bf16 unless out or
     out_dtype says otherwise); accumulate (fp32 out only) adds the product to out."""
-    M, K = _require_matrix(x, FP8, "x")
-    _require_dense(s_x, torch.float32, (M, _blocks(K)), "s_x")
-    N = _fp8_weight(w, s_w, K)
-    out = _fp8_out(out, out_dtype, (M, N), x.device, accumulate, stream)
-    _check(_fn("fp8_block_gemm")(_p(x), _p(s_x), _p(w), _p(s_w), M, N, K, _p(out), TQ_DTYPE[out.dtype],
-                                 int(accumulate), _stream(stream)), "fp8_block_gemm")
+    M, K, dev = _require_matrix(x, FP8, "x")
+    _require_dense(s_x, torch.float32, (M, _blocks(K)), "s_x", dev)
+    N = _fp8_weight(w, s_w, K, dev)
+    out = _fp8_out(out, out_dtype, (M, N), dev, accumulate, stream)
+    _check(_fn("fp8_block_gemm")(x.data_ptr(), s_x.data_ptr(), w.data_ptr(), s_w.data_ptr(), M, N, K, out.data_ptr(),
+                                 TQ_DTYPE[out.dtype], int(accumulate), _raw_stream(stream, dev)), "fp8_block_gemm")
     return out
 
 
@@ -537,12 +548,13 @@ def fp8_block_linear(x: torch.Tensor, w: torch.Tensor, s_w: torch.Tensor, out: O
     """fp8_block_gemm of activations x [M, K] (fp16, bf16 or fp32), which are stored in
     1 x 128 E4M3 blocks on the way (as fp8_block_quantize does)."""
     dt = _float_dtype(x, "x")
-    M, K = _require_matrix(x, x.dtype, "x")
-    N = _fp8_weight(w, s_w, K)
-    out = _fp8_out(out, out_dtype, (M, N), x.device, accumulate, stream)
-    ws = _workspace(ws, fp8_block_linear_workspace_size(M, K), x.device, stream)
-    _check(_fn("fp8_block_linear")(_p(x), dt, _p(w), _p(s_w), M, N, K, _p(out), TQ_DTYPE[out.dtype], int(accumulate),
-                                   _p(ws), ws.numel() * ws.element_size(), _stream(stream)), "fp8_block_linear")
+    M, K, dev = _require_matrix(x, x.dtype, "x")
+    N = _fp8_weight(w, s_w, K, dev)
+    out = _fp8_out(out, out_dtype, (M, N), dev, accumulate, stream)
+    ws = _workspace(ws, fp8_block_linear_workspace_size(M, K), dev, stream)
+    _check(_fn("fp8_block_linear")(x.data_ptr(), dt, w.data_ptr(), s_w.data_ptr(), M, N, K, out.data_ptr(),
+                                   TQ_DTYPE[out.dtype], int(accumulate), ws.data_ptr(),
+                                   ws.numel() * ws.element_size(), _raw_stream(stream, dev)), "fp8_block_linear")
     return out
 
 
@@ -559,26 +571,29 @@ class SwigluSaved:
 
     @staticmethod
     def empty(T: int, D: int, F: int, device="cuda") -> "SwigluSaved":
-        def pair(n):
-            return (torch.empty((T, n), dtype=FP8, device=device),
-                    torch.empty((T, _blocks(n)), dtype=torch.float32, device=device))
-        return SwigluSaved(*pair(D), *pair(F), *pair(F))
+        device = torch.device(device)
+        d, f = _blocks(D), _blocks(F)
+        new = torch.empty
+        return SwigluSaved(new((T, D), dtype=FP8, device=device), new((T, d), dtype=torch.float32, device=device),
+                           new((T, F), dtype=FP8, device=device), new((T, f), dtype=torch.float32, device=device),
+                           new((T, F), dtype=FP8, device=device), new((T, f), dtype=torch.float32, device=device))
 
-    def struct(self, T: int, D: int, F: int) -> TqSwigluSaved:
-        st = TqSwigluSaved()
-        for name, n in (("x", D), ("g", F), ("u", F)):
-            q, s = getattr(self, name), getattr(self, "s_" + name)
-            _require_dense(q, FP8, (T, n), "saved." + name)
-            _require_dense(s, torch.float32, (T, _blocks(n)), "saved.s_" + name)
-            setattr(st, name, q.data_ptr())
-            setattr(st, "s_" + name, s.data_ptr())
-        return st
+    def struct(self, T: int, D: int, F: int, dev: int) -> TqSwigluSaved:
+        d, f = (T, _blocks(D)), (T, _blocks(F))
+        _require_dense(self.x, FP8, (T, D), "saved.x", dev)
+        _require_dense(self.s_x, torch.float32, d, "saved.s_x", dev)
+        _require_dense(self.g, FP8, (T, F), "saved.g", dev)
+        _require_dense(self.s_g, torch.float32, f, "saved.s_g", dev)
+        _require_dense(self.u, FP8, (T, F), "saved.u", dev)
+        _require_dense(self.s_u, torch.float32, f, "saved.s_u", dev)
+        return TqSwigluSaved(self.x.data_ptr(), self.s_x.data_ptr(), self.g.data_ptr(), self.s_g.data_ptr(),
+                             self.u.data_ptr(), self.s_u.data_ptr())
 
 
 def _swiglu_weights(w_gate, w_up, dtype):
-    F, D = _require_matrix(w_gate, dtype, "w_gate")
-    _require_dense(w_up, dtype, (F, D), "w_up")
-    return F, D
+    F, D, dev = _require_matrix(w_gate, dtype, "w_gate")
+    _require_dense(w_up, dtype, w_gate.shape, "w_up", dev)
+    return F, D, dev
 
 
 def swiglu_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, out: Optional[torch.Tensor] = None,
@@ -587,14 +602,14 @@ def swiglu_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, ou
     fp16, D and F multiples of 8; h [T, F].  `saved` receives x and the two projections in
     8 bits for swiglu_backward."""
     dt = _float_dtype(x, "x")
-    T, D = _require_matrix(x, x.dtype, "x")
-    F, wd = _swiglu_weights(w_gate, w_up, x.dtype)
+    T, D, dev = _require_matrix(x, x.dtype, "x")
+    F, wd, _ = _swiglu_weights(w_gate, w_up, x.dtype)
     if wd != D:
         raise ValueError("w_gate has %d inputs, x has %d" % (wd, D))
-    st = saved.struct(T, D, F) if saved is not None else None
-    out = _out(out, (T, F), x.dtype, "out", x.device, stream)
-    _check(_fn("swiglu_forward")(_p(x), _p(w_gate), _p(w_up), dt, T, D, F, _p(out),
-                                 ctypes.byref(st) if st is not None else None, _stream(stream)), "swiglu_forward")
+    st = None if saved is None else saved.struct(T, D, F, dev)
+    out = _out(out, (T, F), x.dtype, "out", dev, stream)
+    _check(_fn("swiglu_forward")(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), dt, T, D, F, out.data_ptr(),
+                                 None if st is None else ctypes.byref(st), _raw_stream(stream, dev)), "swiglu_forward")
     return out
 
 
@@ -611,20 +626,21 @@ def swiglu_backward(dh: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, 
     if (x is None) == (saved is None):
         raise ValueError("swiglu_backward takes exactly one of x and saved")
     dt = _float_dtype(dh, "dh")
-    T, hf = _require_matrix(dh, dh.dtype, "dh")
-    F, D = _swiglu_weights(w_gate, w_up, dh.dtype)
+    T, hf, _ = _require_matrix(dh, dh.dtype, "dh")
+    F, D, dev = _swiglu_weights(w_gate, w_up, dh.dtype)
     if hf != F:
         raise ValueError("dh has %d columns, w_gate has %d outputs" % (hf, F))
     if x is not None:
-        _require_dense(x, dh.dtype, (T, D), "x")
-    st = saved.struct(T, D, F) if saved is not None else None
-    dx = _out(dx, (T, D), dh.dtype, "dx", dh.device, stream)
-    dw_gate = _out(dw_gate, (F, D), dh.dtype, "dw_gate", dh.device, stream)
-    dw_up = _out(dw_up, (F, D), dh.dtype, "dw_up", dh.device, stream)
-    ws = _workspace(ws, swiglu_backward_workspace_size(T, D, F, saved is not None), dh.device, stream)
-    _check(_fn("swiglu_backward")(_p(dh), _p(x), ctypes.byref(st) if st is not None else None, _p(w_gate), _p(w_up),
-                                  dt, T, D, F, _p(dx), _p(dw_gate), _p(dw_up), _p(ws),
-                                  ws.numel() * ws.element_size(), _stream(stream)), "swiglu_backward")
+        _require_dense(x, dh.dtype, (T, D), "x", dev)
+    st = None if saved is None else saved.struct(T, D, F, dev)
+    dx = _out(dx, (T, D), dh.dtype, "dx", dev, stream)
+    dw_gate = _out(dw_gate, (F, D), dh.dtype, "dw_gate", dev, stream)
+    dw_up = _out(dw_up, (F, D), dh.dtype, "dw_up", dev, stream)
+    ws = _workspace(ws, swiglu_backward_workspace_size(T, D, F, saved is not None), dev, stream)
+    _check(_fn("swiglu_backward")(dh.data_ptr(), None if x is None else x.data_ptr(),
+                                  None if st is None else ctypes.byref(st), w_gate.data_ptr(), w_up.data_ptr(), dt, T,
+                                  D, F, dx.data_ptr(), dw_gate.data_ptr(), dw_up.data_ptr(), ws.data_ptr(),
+                                  ws.numel() * ws.element_size(), _raw_stream(stream, dev)), "swiglu_backward")
     return dx, dw_gate, dw_up
 
 

@@ -45,8 +45,12 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
     return v;
 }
 
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// Arrival on a barrier of another CTA that hands over tensor memory which this thread has
+// finished reading (its loads waited for): no generic memory is handed over, so it needs no
+// release, whose cluster-wide fence stalled the accumulator loop (309 -> XXX us, 8192 x 4096
+// x 4096 E4M3).
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // ------------------------------------------------------------------------------ CTA pair
@@ -179,6 +183,23 @@ __device__ __forceinline__ void e4m3x4_to_f32(uint32_t q, float (&v)[4]) {
     v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
 }
 
+// ------------------------------------------------------------------------------ fp32 pairs
+
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ float f32x2_lo(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float f32x2_hi(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+
+// acc += f * (lo, hi): two fp32 FMAs (nearest even) in one instruction.
+__device__ __forceinline__ void fma_f32x2(uint64_t &acc, uint64_t f, uint32_t lo, uint32_t hi) {
+    asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%2, %3};\n\tfma.rn.f32x2 %0, %1, v, %0;\n\t}"
+        : "+l"(acc)
+        : "l"(f), "r"(lo), "r"(hi));
+}
+
 // ------------------------------------------------------------------------------ 16-bit packing
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -190,6 +211,63 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
     return *reinterpret_cast<uint32_t *>(&v);
 }
 __device__ __forceinline__ uint32_t pack16(float a, float b, bool f16) { return f16 ? pack_f16(a, b) : pack_bf16(a, b); }
+
+// ------------------------------------------------------------------------------ row stores
+
+// An accumulator thread holds a row, so its own stores would touch 32 rows an instruction
+// and write a 32-byte sector in two to four pieces.  A warp instead passes 32 rows x 128
+// bytes through shared memory (rows 144 bytes apart: no bank conflicts) and stores four
+// whole 128-byte row pieces an instruction.
+constexpr int kRowStage = 32 * 144;      // bytes a warp
+
+// v: the lane's row (row `lane` of 32, 128 bytes); out: the warp's first row at its first
+// byte; row_bytes: distance of rows; rows, bytes: how many of the 32 rows and 128 bytes exist.
+// vec16: row_bytes and out are multiples of 16 (bytes then is, too).  ELEM: bytes of an
+// element, stored one by one otherwise.  accumulate (fp32): add to what is there.
+template <int ELEM>
+__device__ __forceinline__ void warp_store_rows(unsigned char *stage, int lane, const uint4 (&v)[8], char *out,
+                                                size_t row_bytes, int rows, int bytes, bool vec16,
+                                                bool accumulate = false) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4 *>(stage + lane * 144 + 16 * i) = v[i];
+    __syncwarp();
+    if (vec16) {
+        const int c = (lane & 7) * 16;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3);
+            if (r < rows && c < bytes) {
+                uint4 w = *reinterpret_cast<const uint4 *>(stage + r * 144 + c);
+                uint4 *p = reinterpret_cast<uint4 *>(out + (size_t)r * row_bytes + c);
+                if (ELEM == 4 && accumulate) {
+                    const float4 o = *reinterpret_cast<const float4 *>(p);
+                    w.x = __float_as_uint(__uint_as_float(w.x) + o.x);
+                    w.y = __float_as_uint(__uint_as_float(w.y) + o.y);
+                    w.z = __float_as_uint(__uint_as_float(w.z) + o.z);
+                    w.w = __float_as_uint(__uint_as_float(w.w) + o.w);
+                }
+                *p = w;
+            }
+        }
+    } else {
+        constexpr int kPer = 128 / ELEM;
+#pragma unroll 4
+        for (int e = lane; e < 32 * kPer; e += 32) {
+            const int r = e / kPer, c = (e % kPer) * ELEM;
+            if (r < rows && c < bytes) {
+                char *p = out + (size_t)r * row_bytes + c;
+                if (ELEM == 4) {
+                    const float f = *reinterpret_cast<const float *>(stage + r * 144 + c);
+                    float *q = reinterpret_cast<float *>(p);
+                    *q = accumulate ? *q + f : f;
+                } else {
+                    *reinterpret_cast<uint16_t *>(p) = *reinterpret_cast<const uint16_t *>(stage + r * 144 + c);
+                }
+            }
+        }
+    }
+    __syncwarp();
+}
 
 // ------------------------------------------------------------------------------ SwiGLU
 

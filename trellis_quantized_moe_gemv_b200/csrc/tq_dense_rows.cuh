@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(kRowsThreads, KIND == kFp8 && N > 64 ? 1 : 2)
     chain_entry();
 
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        if (mbar_try_wait(bar, parity)) return true;
         if (*(volatile int32_t *)&sm.abort) return false;
         const bool ok = mbar_wait_sleep(bar, parity);
         if (!ok) sm.abort = 1;

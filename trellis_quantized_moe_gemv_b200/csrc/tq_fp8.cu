@@ -147,13 +147,14 @@ __global__ void __launch_bounds__(256) fp8_dequantize_kernel(const uint8_t *__re
 
 // ------------------------------------------------------------------------------ product
 
-constexpr int kFp8Stages = 6;
+constexpr int kFp8Stages = 5;
 constexpr int kFp8Threads = 384;       // warp 0 TMA, 1 MMA (leader), 2 TMEM, 4-11 epilogue
 constexpr int kFp8StageBytes = 16384;  // 128 rows x 128 E4M3
 
 struct __align__(1024) Fp8Smem {
     unsigned char a[kFp8Stages][kFp8StageBytes];
     unsigned char b[kFp8Stages][kFp8StageBytes];
+    unsigned char rows[8][kRowStage];
     uint64_t full[kFp8Stages];      // leader: both CTAs' copies of the stage
     uint64_t empty[kFp8Stages];     // MMA commit, in both CTAs
     uint64_t acc_full[2];           // MMA commit, in both CTAs
@@ -197,16 +198,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8Threads, 1)
     chain_entry();
 
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        if (mbar_try_wait(bar, parity)) return true;
         if (*(volatile int32_t *)&sm.abort) return false;
         const bool ok = mbar_wait_sleep(bar, parity);
         if (!ok) sm.abort = 1;
         return ok;
     };
 
-    // Registers: 384 threads are launched with 168 each (64,512); 4 warps of 80 and 8 of 208
-    // are 63,488.
+    // Registers: 384 threads are launched with 168 each (64,512); 4 warps of 56 and 8 of 224
+    // are 64,512.
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 0 && lane == 0) {
             bool ok = true;
             uint32_t it = 0;
@@ -252,7 +254,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8Threads, 1)
             }
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
         const int q = warp & 3, w = (warp - 4) >> 2;
         const int row = 128 * rank + 32 * q + lane;
         const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16) + 128 * w;
@@ -266,47 +268,80 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8Threads, 1)
             const bool mine = r < args.rows && nb < n_blocks;
             const float *sx = args.sx + (size_t)(mine ? r : 0) * nkb;
             const float *sw = args.sw + (size_t)(mine ? nb : 0) * nkb;
-            float acc[128];
+            uint64_t acc[64];          // pairs of columns
 #pragma unroll
-            for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-            float next = mine ? sx[0] * sw[0] : 0.f;
+            for (int i = 0; i < 64; ++i) acc[i] = 0;
+            // the block's scales are loaded one block ahead and multiplied when used
+            float next_x = mine ? sx[0] : 0.f, next_w = mine ? sw[0] : 0.f;
             for (int kb = 0; kb < nkb; ++kb, ++it) {
                 const uint32_t st = it & 1;
-                const float f = next;
-                if (kb + 1 < nkb) next = mine ? sx[kb + 1] * sw[kb + 1] : 0.f;
+                const float f1 = next_x * next_w;
+                const uint64_t f = f32x2(f1, f1);
+                if (mine && kb + 1 < nkb) {
+                    next_x = sx[kb + 1];
+                    next_w = sw[kb + 1];
+                }
                 ok = __all_sync(0xffffffffu, wait(&sm.acc_full[st], (it >> 1) & 1));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t at = taddr + st * 256;
                 uint32_t a[32], b[32];
+                // two loads in flight a wait: a load's latency, not its bandwidth, is what a
+                // warp waits for
                 tmem_ld32(at, a);
-                tmem_ld_wait();
                 tmem_ld32(at + 32, b);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) acc[i] = fmaf(f, __uint_as_float(a[i]), acc[i]);
                 tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) fma_f32x2(acc[i], f, a[2 * i], a[2 * i + 1]);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) fma_f32x2(acc[16 + i], f, b[2 * i], b[2 * i + 1]);
                 tmem_ld32(at + 64, a);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) acc[32 + i] = fmaf(f, __uint_as_float(b[i]), acc[32 + i]);
-                tmem_ld_wait();
                 tmem_ld32(at + 96, b);
-#pragma unroll
-                for (int i = 0; i < 32; ++i) acc[64 + i] = fmaf(f, __uint_as_float(a[i]), acc[64 + i]);
                 tmem_ld_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&sm.acc_empty[st]), 0));
+                if (lane == 0) mbar_arrive_cluster_relaxed(map_to_rank(smem_u32(&sm.acc_empty[st]), 0));
 #pragma unroll
-                for (int i = 0; i < 32; ++i) acc[96 + i] = fmaf(f, __uint_as_float(b[i]), acc[96 + i]);
+                for (int i = 0; i < 16; ++i) fma_f32x2(acc[32 + i], f, a[2 * i], a[2 * i + 1]);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) fma_f32x2(acc[48 + i], f, b[2 * i], b[2 * i + 1]);
             }
-            if (ok && r < args.rows) {
-                const int col = n * 256 + 128 * w;
+            if (!ok) break;
+            // the warp's 32 rows x 128 columns, 128 bytes of each row at a time
+            const int col = n * 256 + 128 * w, row0 = m * 256 + 128 * rank + 32 * q;
+            const int es = args.out_type == TQ_DTYPE_F32 ? 4 : 2;
+            const size_t row_bytes = (size_t)args.width * es;
+            const bool vec16 = row_bytes % 16 == 0;
+            char *out = reinterpret_cast<char *>(args.out) + (size_t)row0 * row_bytes + (size_t)col * es;
+            const int bytes = (args.width - col < 128 ? args.width - col : 128) * es, rows = args.rows - row0;
+            uint4 v[8];
+            if (es == 4) {
 #pragma unroll
-                for (int c = 0; c < 128; c += 4) {
-                    const float v[4] = {acc[c], acc[c + 1], acc[c + 2], acc[c + 3]};
-                    if (col + c < args.width)
-                        store_out4(args.out, (size_t)r * args.width + col + c, v, min(4, args.width - col - c),
-                                   args.out_type, args.accumulate != 0);
+                for (int c = 0; c < 4; ++c) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint64_t x = acc[16 * c + 2 * i], y = acc[16 * c + 2 * i + 1];
+                        v[i] = make_uint4((uint32_t)x, (uint32_t)(x >> 32), (uint32_t)y, (uint32_t)(y >> 32));
+                    }
+                    warp_store_rows<4>(sm.rows[warp - 4], lane, v, out + 128 * c, row_bytes, rows, bytes - 128 * c,
+                                       vec16, args.accumulate != 0);
+                }
+            } else {
+                const bool f16 = args.out_type == TQ_DTYPE_F16;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        uint32_t p[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint64_t x = acc[32 * c + 4 * i + j];
+                            p[j] = pack16(f32x2_lo(x), f32x2_hi(x), f16);
+                        }
+                        v[i] = make_uint4(p[0], p[1], p[2], p[3]);
+                    }
+                    warp_store_rows<2>(sm.rows[warp - 4], lane, v, out + 128 * c, row_bytes, rows, bytes - 128 * c,
+                                       vec16);
                 }
             }
         }

@@ -7,7 +7,7 @@
 // Three products, all by one persistent CTA-pair kernel (tcgen05, cta_group::2): a pair
 // owns a 256 x 256 tile of fp32 accumulators, each CTA its 128 rows in its own tensor
 // memory (two tiles of 256 columns: the epilogue of one tile runs under the MMAs of the
-// next).  Per K-block of 64 each CTA brings in its half of both operands (2 x 16 KB, 6
+// next).  Per K-block of 64 each CTA brings in its half of both operands (2 x 16 KB, 5
 // stages) by TMA; the leader's MMA thread issues 4 MMAs of 256 x 256 x 16.
 //   * gate/up: the B operand's first half is 128 gate rows (CTA 0), its second half the
 //     same 128 up rows (CTA 1), so a row's g and u meet in one thread's epilogue, which
@@ -27,13 +27,14 @@
 namespace tq {
 
 constexpr int kPairM = 256, kPairN = 256;
-constexpr int kPairStages = 6;
+constexpr int kPairStages = 5;
 constexpr int kPairThreads = 384;      // warp 0 TMA, 1 MMA (leader), 2 TMEM, 4-11 epilogue
 constexpr int kPairStageBytes = 16384;
 
 struct __align__(1024) PairSmem {
     unsigned char a[kPairStages][kPairStageBytes];
     unsigned char b[kPairStages][kPairStageBytes];
+    unsigned char rows[8][kRowStage];
     uint64_t full[kPairStages];     // leader: both CTAs' copies of the stage
     uint64_t empty[kPairStages];    // MMA commit, in both CTAs
     uint64_t acc_full[2];           // MMA commit, in both CTAs
@@ -107,68 +108,83 @@ __device__ __forceinline__ PairTile pair_tile(const PairArgs &p, long long t) {
 
 // ------------------------------------------------------------------------------ epilogues
 
-__device__ __forceinline__ void store_row16(void *base, size_t i, const float *v, int n, bool f16) {
-    uint4 *p = reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(base) + i);
+// 32 fp32 values of a row as 64 bytes of 16-bit values.
+__device__ __forceinline__ void pack_row32(const float (&v)[32], bool f16, uint4 *p) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        if (8 * j < n)
-            p[j] = make_uint4(pack16(v[8 * j], v[8 * j + 1], f16), pack16(v[8 * j + 2], v[8 * j + 3], f16),
-                              pack16(v[8 * j + 4], v[8 * j + 5], f16), pack16(v[8 * j + 6], v[8 * j + 7], f16));
+        p[j] = make_uint4(pack16(v[8 * j], v[8 * j + 1], f16), pack16(v[8 * j + 2], v[8 * j + 3], f16),
+                          pack16(v[8 * j + 4], v[8 * j + 5], f16), pack16(v[8 * j + 6], v[8 * j + 7], f16));
 }
 
-// One warp's share of a tile: tensor-memory lane quarter q (rows), column half w.
+// One warp's share of a tile: rows row0 .. row0 + 31 of the tile (tensor-memory lane quarter
+// taddr), column half w.  `stage`: the warp's row stage.
 template <int KIND>
-__device__ __forceinline__ void pair_epilogue(const PairArgs &p, const PairTile &t, uint32_t taddr, int row, int w) {
+__device__ __forceinline__ void pair_epilogue(const PairArgs &p, const PairTile &t, uint32_t taddr, int row0, int lane,
+                                              int w, unsigned char *stage) {
     uint32_t a[32], b[32];
     float v[32];
+    uint4 o[8];
+    const int r0 = t.m0 + row0;
     if constexpr (KIND == kPairGrads) {
         __nv_bfloat16 *out = t.which < 0 ? p.dx : (t.which ? p.dwu : p.dwg);
-        const int rows = t.which < 0 ? p.T : p.F;
-        const int r = t.m0 + row;
+        const int rows = (t.which < 0 ? p.T : p.F) - r0;
 #pragma unroll 1
-        for (int c = 128 * w; c < 128 * w + 128; c += 32) {
+        for (int c = 128 * w; c < 128 * w + 128; c += 64) {
             tmem_ld32(taddr + c, a);
+            tmem_ld32(taddr + c + 32, b);
             tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(a[i]);
+            pack_row32(v, false, o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(b[i]);
+            pack_row32(v, false, o + 4);
             const int col = t.n0 + c;
-            if (r < rows) store_row16(out, (size_t)r * p.D + col, v, p.D - col, false);
+            warp_store_rows<2>(stage, lane, o, reinterpret_cast<char *>(out + (size_t)r0 * p.D + col), (size_t)p.D * 2,
+                               rows, (p.D - col) * 2, true);
         }
         return;
     }
-    const int r = t.m0 + row;
+    const int r = r0 + lane, rows = p.T - r0;
     if constexpr (KIND == kPairSave) {
         // column half w stores matrix w (0: g, 1: u) of the 128-wide block in 8 bits
         const uint32_t m_addr = taddr + 128 * w;
         float m = 0.f;
 #pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
+        for (int c = 0; c < 128; c += 64) {
             tmem_ld32(m_addr + c, a);
+            tmem_ld32(m_addr + c + 32, b);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) m = finite_max(m, __uint_as_float(a[i]));   // columns past F hold zeros
+            for (int i = 0; i < 32; ++i)     // columns past F hold zeros
+                m = finite_max(finite_max(m, __uint_as_float(a[i])), __uint_as_float(b[i]));
         }
         const int e = e4m3_block_exponent(m);
         const float inv = exp2_int(-e);
         const int fb = (p.F + 127) / 128;
         if (r < p.T) (w ? p.su : p.sg)[(size_t)r * fb + t.n0 / 128] = exp2_int(e);
-        uint8_t *q = (w ? p.u8 : p.g8) + (size_t)r * p.F + t.n0;
-#pragma unroll 1
+#pragma unroll
         for (int c = 0; c < 128; c += 32) {
             tmem_ld32(m_addr + c, a);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; i += 8) {
-                const uint32_t lo = e4m3x4_scaled(__uint_as_float(a[i]), __uint_as_float(a[i + 1]),
-                                                  __uint_as_float(a[i + 2]), __uint_as_float(a[i + 3]), inv);
-                const uint32_t hi = e4m3x4_scaled(__uint_as_float(a[i + 4]), __uint_as_float(a[i + 5]),
-                                                  __uint_as_float(a[i + 6]), __uint_as_float(a[i + 7]), inv);
-                if (r < p.T && t.n0 + c + i < p.F) *reinterpret_cast<uint2 *>(q + c + i) = make_uint2(lo, hi);
+            for (int i = 0; i < 32; i += 16) {
+                uint32_t q[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    q[j] = e4m3x4_scaled(__uint_as_float(a[i + 4 * j]), __uint_as_float(a[i + 4 * j + 1]),
+                                         __uint_as_float(a[i + 4 * j + 2]), __uint_as_float(a[i + 4 * j + 3]), inv);
+                o[(c + i) / 16] = make_uint4(q[0], q[1], q[2], q[3]);
             }
         }
+        // F % 16 == 8: rows are 8-byte aligned, stored in 2-byte pieces
+        warp_store_rows<2>(stage, lane, o, reinterpret_cast<char *>((w ? p.u8 : p.g8) + (size_t)r0 * p.F + t.n0),
+                           (size_t)p.F, rows, p.F - t.n0, p.F % 16 == 0);
     }
-#pragma unroll 1
-    for (int c = 64 * w; c < 64 * w + 64; c += 32) {
+    uint4 o2[8];     // du (backward)
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int c = 64 * w + 32 * half;
         tmem_ld32(taddr + c, a);
         tmem_ld32(taddr + 128 + c, b);
         const int col = t.n0 + c;
@@ -187,16 +203,25 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs &p, const PairTile 
                 const float dh = __uint_as_float((i & 1) ? (w2 & 0xFFFF0000u) : (w2 << 16));
                 swiglu_grads(__uint_as_float(a[i]), __uint_as_float(b[i]), dh, v[i], du[i]);
             }
-            if (r < p.T) {
-                store_row16(p.dg, (size_t)r * p.F + col, v, p.F - col, false);
-                store_row16(p.du, (size_t)r * p.F + col, du, p.F - col, false);
-            }
+            pack_row32(v, false, o + 4 * half);
+            pack_row32(du, false, o2 + 4 * half);
         } else {
             tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = swiglu_value(__uint_as_float(a[i]), __uint_as_float(b[i]));
-            if (r < p.T) store_row16(p.h, (size_t)r * p.F + col, v, p.F - col, p.f16 != 0);
+            pack_row32(v, p.f16 != 0, o + 4 * half);
         }
+    }
+    const int col = t.n0 + 64 * w;
+    const size_t at = (size_t)r0 * p.F + col;
+    if constexpr (KIND == kPairRecompute) {
+        warp_store_rows<2>(stage, lane, o, reinterpret_cast<char *>(p.dg + at), (size_t)p.F * 2, rows, (p.F - col) * 2,
+                           true);
+        warp_store_rows<2>(stage, lane, o2, reinterpret_cast<char *>(p.du + at), (size_t)p.F * 2, rows, (p.F - col) * 2,
+                           true);
+    } else {
+        warp_store_rows<2>(stage, lane, o, reinterpret_cast<char *>(p.h) + at * 2, (size_t)p.F * 2, rows,
+                           (p.F - col) * 2, true);
     }
 }
 
@@ -234,6 +259,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     chain_entry();
 
     auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
+        if (mbar_try_wait(bar, parity)) return true;
         if (*(volatile int32_t *)&sm.abort) return false;
         const bool ok = mbar_wait_sleep(bar, parity);
         if (!ok) sm.abort = 1;
@@ -316,7 +342,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
     } else if (warp >= 4) {
         const int q = warp & 3, w = (warp - 4) >> 2;
-        const int row = 128 * rank + 32 * q + lane;
         uint32_t j = 0;
         for (long long t = pair; t < tiles; t += pairs, ++j) {
             const PairTile tl = pair_tile<KIND>(args, t);
@@ -324,10 +349,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             const bool ok = __all_sync(0xffffffffu, wait(&sm.acc_full[st], (j >> 1) & 1));
             if (!ok) break;
             tc_fence_after();
-            pair_epilogue<KIND>(args, tl, tmem + st * kPairN + ((uint32_t)(32 * q) << 16), row, w);
+            pair_epilogue<KIND>(args, tl, tmem + st * kPairN + ((uint32_t)(32 * q) << 16), 128 * rank + 32 * q, lane, w,
+                                sm.rows[warp - 4]);
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(map_to_rank(smem_u32(&sm.acc_empty[st]), 0));
+            if (lane == 0) mbar_arrive_cluster_relaxed(map_to_rank(smem_u32(&sm.acc_empty[st]), 0));
         }
     }
     __syncwarp();
