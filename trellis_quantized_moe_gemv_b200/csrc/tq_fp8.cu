@@ -40,37 +40,53 @@ __device__ __forceinline__ void load8(const T *p, float (&v)[8]) {
     }
 }
 
-// 1 x 128 blocks: 16 lanes hold a block (8 values each), so a row's values are read once
-// and its largest magnitude takes 4 exchanges.  Memory-bound.
+// Row kernels: a warp takes kStoreRows rows of 512 columns (4 blocks), 16 lanes a block,
+// 8 values a lane; blockIdx.y is the group of 512 columns, so no index is divided.  All
+// loads of a warp are in flight together (4 a lane), which the reads from HBM need.
+constexpr int kStoreRows = 2;
+constexpr int kStoreWarps = 8;
+
+// 1 x 128 blocks: a row's values are read once and its largest magnitude takes 4 exchanges.
+// Memory-bound.
 template <typename T>
-__global__ void __launch_bounds__(256) fp8_quantize_rows_kernel(const T *__restrict__ x, long long rows, int cols,
-                                                                uint8_t *__restrict__ out,
-                                                                float *__restrict__ scales) {
+__global__ void __launch_bounds__(kStoreWarps * 32) fp8_quantize_rows_kernel(const T *__restrict__ x, long long rows,
+                                                                            int cols, uint8_t *__restrict__ out,
+                                                                            float *__restrict__ scales) {
     chain_entry();
     const int nb = (cols + 127) / 128;
-    const long long n = rows * nb;
-    const int sub = threadIdx.x & 15;
-    // both halves of a warp take the same number of steps (the exchanges are warp-wide)
-    for (long long i0 = (blockIdx.x * 256LL + threadIdx.x) / 32 * 2; i0 < n; i0 += gridDim.x * 16LL) {
-        const long long i = i0 + ((threadIdx.x >> 4) & 1);
-        const long long r = i < n ? i / nb : 0;
-        const int b = i < n ? (int)(i - r * nb) : 0;
-        const int c = b * 128 + sub * 8;
-        const bool in = i < n && c < cols;
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (in) load8<T>(x + (size_t)r * cols + c, v);
-        float m = 0.f;
+    const int lane = threadIdx.x & 31;
+    const long long r0 = ((long long)blockIdx.x * kStoreWarps + (threadIdx.x >> 5)) * kStoreRows;
+    const int c0 = blockIdx.y * 512 + lane * 8;
+    float v[kStoreRows][2][8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = finite_max(m, v[j]);
+    for (int k = 0; k < kStoreRows; ++k)
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const int e = e4m3_block_exponent(m);
-        const float inv = exp2_int(-e);
-        if (in)
-            *reinterpret_cast<uint2 *>(out + (size_t)r * cols + c) =
-                make_uint2(e4m3x4_scaled(v[0], v[1], v[2], v[3], inv), e4m3x4_scaled(v[4], v[5], v[6], v[7], inv));
-        if (sub == 0 && i < n) scales[(size_t)r * nb + b] = exp2_int(e);
-    }
+        for (int h = 0; h < 2; ++h) {
+            const int c = c0 + 256 * h;
+            if (r0 + k < rows && c < cols) load8<T>(x + (size_t)(r0 + k) * cols + c, v[k][h]);
+            else
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[k][h][j] = 0.f;
+        }
+#pragma unroll
+    for (int k = 0; k < kStoreRows; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = c0 + 256 * h;
+            const float *w = v[k][h];
+            float m = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) m = finite_max(m, w[j]);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const int e = e4m3_block_exponent(m);
+            const float inv = exp2_int(-e);
+            if (r0 + k < rows && c < cols) {
+                *reinterpret_cast<uint2 *>(out + (size_t)(r0 + k) * cols + c) =
+                    make_uint2(e4m3x4_scaled(w[0], w[1], w[2], w[3], inv), e4m3x4_scaled(w[4], w[5], w[6], w[7], inv));
+                if ((lane & 15) == 0) scales[(size_t)(r0 + k) * nb + c / 128] = exp2_int(e);
+            }
+        }
 }
 
 // 128 x 128 blocks: one CTA a block, 64 values a thread kept in registers.
@@ -114,35 +130,50 @@ __global__ void __launch_bounds__(256) fp8_quantize_blocks_kernel(const T *__res
     }
 }
 
-// Stored values times their scales: 8 values a thread.  Memory-bound.
-__global__ void __launch_bounds__(256) fp8_dequantize_kernel(const uint8_t *__restrict__ q,
-                                                             const float *__restrict__ scales, long long rows, int cols,
-                                                             int block_rows, void *__restrict__ out, int type) {
+// Stored values times their scales, laid out over warps as the row kernel above.  Memory-bound.
+__global__ void __launch_bounds__(kStoreWarps * 32) fp8_dequantize_kernel(const uint8_t *__restrict__ q,
+                                                                         const float *__restrict__ scales,
+                                                                         long long rows, int cols, int block_rows,
+                                                                         void *__restrict__ out, int type) {
     chain_entry();
-    const int nb = (cols + 127) / 128, per_row = cols / 8;
-    const long long n = rows * per_row;
-    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < n; i += gridDim.x * 256LL) {
-        const long long r = i / per_row;
-        const int c = (int)(i - r * per_row) * 8;
-        const uint2 w = *reinterpret_cast<const uint2 *>(q + (size_t)r * cols + c);
-        const float s = scales[(size_t)(r / block_rows) * nb + c / 128];
-        float v[8];
-        e4m3x4_to_f32(w.x, *reinterpret_cast<float(*)[4]>(v));
-        e4m3x4_to_f32(w.y, *reinterpret_cast<float(*)[4]>(v + 4));
+    const int nb = (cols + 127) / 128;
+    const long long r0 = ((long long)blockIdx.x * kStoreWarps + (threadIdx.x >> 5)) * kStoreRows;
+    const int c0 = blockIdx.y * 512 + (threadIdx.x & 31) * 8;
+    uint2 w[kStoreRows][2];
+    float s[kStoreRows][2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= s;
-        const size_t at = (size_t)r * cols + c;
-        if (type == TQ_DTYPE_F32) {
-            float4 *p = reinterpret_cast<float4 *>(reinterpret_cast<float *>(out) + at);
-            p[0] = make_float4(v[0], v[1], v[2], v[3]);
-            p[1] = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
-            const bool f16 = type == TQ_DTYPE_F16;
-            *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(out) + at) =
-                make_uint4(pack16(v[0], v[1], f16), pack16(v[2], v[3], f16), pack16(v[4], v[5], f16),
-                           pack16(v[6], v[7], f16));
+    for (int k = 0; k < kStoreRows; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = c0 + 256 * h;
+            if (r0 + k < rows && c < cols) {
+                w[k][h] = *reinterpret_cast<const uint2 *>(q + (size_t)(r0 + k) * cols + c);
+                s[k][h] = scales[(size_t)(block_rows == 1 ? r0 + k : (r0 + k) / 128) * nb + c / 128];
+            }
         }
-    }
+#pragma unroll
+    for (int k = 0; k < kStoreRows; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = c0 + 256 * h;
+            if (r0 + k >= rows || c >= cols) continue;
+            float v[8];
+            e4m3x4_to_f32(w[k][h].x, *reinterpret_cast<float(*)[4]>(v));
+            e4m3x4_to_f32(w[k][h].y, *reinterpret_cast<float(*)[4]>(v + 4));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] *= s[k][h];
+            const size_t at = (size_t)(r0 + k) * cols + c;
+            if (type == TQ_DTYPE_F32) {
+                float4 *p = reinterpret_cast<float4 *>(reinterpret_cast<float *>(out) + at);
+                p[0] = make_float4(v[0], v[1], v[2], v[3]);
+                p[1] = make_float4(v[4], v[5], v[6], v[7]);
+            } else {
+                const bool f16 = type == TQ_DTYPE_F16;
+                *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(out) + at) =
+                    make_uint4(pack16(v[0], v[1], f16), pack16(v[2], v[3], f16), pack16(v[4], v[5], f16),
+                               pack16(v[6], v[7], f16));
+            }
+        }
 }
 
 // ------------------------------------------------------------------------------ product
@@ -413,17 +444,22 @@ static int fp8_product_status(int M, int N, int K, int y_dtype, int accumulate) 
     return TQ_OK;
 }
 
-static unsigned capped_blocks(long long blocks) {
-    const long long most = 8LL * num_sms();
-    return (unsigned)(blocks < most ? blocks : most);
+// Grid of the row kernels, and whether it is one.
+static dim3 store_grid(long long rows, int cols) {
+    const long long per = kStoreWarps * kStoreRows;
+    return dim3((unsigned)((rows + per - 1) / per), (unsigned)((cols + 511) / 512));
+}
+static bool store_grid_fits(long long rows, int cols) {
+    return rows <= 0x7FFFFFFFLL * kStoreWarps * kStoreRows && ((long long)cols + 511) / 512 <= 65535;
 }
 
 template <typename T>
 static cudaError_t quantize_launch(const void *x, long long rows, int cols, int block_rows, uint8_t *out, float *scales,
                                    cudaStream_t s) {
-    const long long nb = (cols + 127) / 128;
+    const long long nb = (cols + 127LL) / 128;
     if (block_rows == 1)
-        return launch_chained(fp8_quantize_rows_kernel<T>, dim3(capped_blocks((rows * nb + 15) / 16)), dim3(256), 0, s,
+        return launch_chained(fp8_quantize_rows_kernel<T>, store_grid(rows, cols),
+                              dim3(kStoreWarps * 32), 0, s,
                               (const T *)x, rows, cols, out, scales);
     return launch_chained(fp8_quantize_blocks_kernel<T>, dim3((unsigned)((rows + 127) / 128 * nb)), dim3(256), 0, s,
                           (const T *)x, rows, cols, out, scales);
@@ -438,7 +474,8 @@ TQ_API int fp8_block_quantize(const void *x, int x_dtype, int64_t rows, int cols
         (block_rows != 1 && block_rows != 128))
         return TQ_ERR_INVALID_ARG;
     if (rows == 0) return TQ_OK;
-    if (block_rows == 128 && (rows + 127) / 128 * ((cols + 127) / 128) > 0x7FFFFFFFLL) return TQ_ERR_UNSUPPORTED;
+    if (block_rows == 128 ? (rows + 127) / 128 * ((cols + 127LL) / 128) > 0x7FFFFFFFLL : !store_grid_fits(rows, cols))
+        return TQ_ERR_UNSUPPORTED;
     if (!x || !out || !scales) return TQ_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned16(out) || !aligned16(scales)) return TQ_ERR_ALIGNMENT;
     const cudaStream_t s = (cudaStream_t)stream;
@@ -456,13 +493,13 @@ TQ_API int fp8_block_dequantize(const uint8_t *q, const float *scales, int64_t r
         (block_rows != 1 && block_rows != 128))
         return TQ_ERR_INVALID_ARG;
     if (rows == 0) return TQ_OK;
+    if (!store_grid_fits(rows, cols)) return TQ_ERR_UNSUPPORTED;
     if (!q || !scales || !out) return TQ_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(scales) || !aligned16(out)) return TQ_ERR_ALIGNMENT;
     const cudaStream_t s = (cudaStream_t)stream;
     LaunchScope ls(s, kStageFp8Store);
-    const long long blocks = ((long long)rows * (cols / 8) + 255) / 256;
-    if (launch_chained(fp8_dequantize_kernel, dim3(capped_blocks(blocks)), dim3(256), 0, s, q, scales, (long long)rows,
-                       cols, block_rows, out, out_dtype) != cudaSuccess)
+    if (launch_chained(fp8_dequantize_kernel, store_grid(rows, cols), dim3(kStoreWarps * 32), 0, s, q, scales,
+                       (long long)rows, cols, block_rows, out, out_dtype) != cudaSuccess)
         return record_cuda_error("fp8_block_dequantize");
     return launch_status();
 }
