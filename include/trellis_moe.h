@@ -337,11 +337,13 @@ int fp8_block_dequantize(const uint8_t *q, const float *scales, int64_t rows, in
  *   K % 16 == 0; M and N any size; all arrays 16-byte aligned.
  * fp8_block_linear -- the same from activations x [M][K] of x_dtype (F16, BF16 or F32),
  * which are quantised as fp8_block_quantize (block_rows 1) does on the way.  ws: device
- * workspace of fp8_block_linear_workspace_size(M, K) bytes, 16-byte aligned.
+ * workspace of fp8_block_linear_workspace_size(M, N, K) bytes, 16-byte aligned; 0 bytes (ws
+ * may be NULL) for products of few rows (up to 16), which one kernel quantises and multiplies.
+ * The size depends on the device's SM count: query it on the device that runs the call.
  */
 int fp8_block_gemm(const uint8_t *x, const float *s_x, const uint8_t *w, const float *s_w, int M, int N, int K,
                    void *y, int y_dtype, int accumulate, tq_stream stream);
-size_t fp8_block_linear_workspace_size(int M, int K);
+size_t fp8_block_linear_workspace_size(int M, int N, int K);
 int fp8_block_linear(const void *x, int x_dtype, const uint8_t *w, const float *s_w, int M, int N, int K,
                      void *y, int y_dtype, int accumulate, void *ws, size_t ws_bytes, tq_stream stream);
 

@@ -60,17 +60,19 @@ def test_products(lib):
     assert g(FAKE, FAKE, MISALIGNED, FAKE, 4, 4, 128, FAKE, F32, 0, None) == ALIGNMENT
     assert g(None, None, None, None, 0, 4, 128, None, F32, 0, None) == OK
     assert g(None, None, None, None, 4, 0, 128, None, F32, 0, None) == OK
-    need = lib.fp8_block_linear_workspace_size(5, 144)
-    assert need == 768 + 256             # 5 x 144 E4M3 bytes and 5 x 2 scales, in units of 256
-    assert lib.fp8_block_linear_workspace_size(5, 100) == 0
+    need = lib.fp8_block_linear_workspace_size(33, 4, 144)
+    assert need == 4864 + 512            # 33 x 144 E4M3 bytes and 33 x 2 scales, in units of 256
+    assert lib.fp8_block_linear_workspace_size(16, 4, 144) == 0      # one kernel
+    assert lib.fp8_block_linear_workspace_size(16, 64 * 1024, 1 << 20) > 0   # its share of K does not fit a CTA
+    assert lib.fp8_block_linear_workspace_size(33, 4, 100) == 0
     lin = lib.fp8_block_linear      # x, dtype, w, s_w, M, N, K, y, y_dtype, accumulate, ws, bytes, stream
-    assert lin(FAKE, 3, FAKE, FAKE, 5, 4, 144, FAKE, F32, 0, FAKE, BIG, None) == INVALID
-    assert lin(FAKE, F32, FAKE, FAKE, 5, 4, 144, FAKE, F32, 0, FAKE, ctypes.c_size_t(need - 1), None) == WORKSPACE
-    assert lin(FAKE, F32, FAKE, FAKE, 5, 4, 144, FAKE, F32, 0, None, BIG, None) == WORKSPACE
-    assert lin(FAKE, F32, FAKE, FAKE, 5, 4, 144, FAKE, F32, 0, MISALIGNED, BIG, None) == ALIGNMENT
-    assert lin(MISALIGNED, F32, FAKE, FAKE, 5, 4, 144, FAKE, F32, 0, FAKE, BIG, None) == ALIGNMENT
-    assert lin(FAKE, F32, FAKE, None, 5, 4, 144, FAKE, F32, 0, FAKE, BIG, None) == INVALID
-    assert lin(FAKE, F32, FAKE, FAKE, 5, 4, 144, FAKE, F16, 1, FAKE, BIG, None) == UNSUPPORTED
+    assert lin(FAKE, 3, FAKE, FAKE, 33, 4, 144, FAKE, F32, 0, FAKE, BIG, None) == INVALID
+    assert lin(FAKE, F32, FAKE, FAKE, 33, 4, 144, FAKE, F32, 0, FAKE, ctypes.c_size_t(need - 1), None) == WORKSPACE
+    assert lin(FAKE, F32, FAKE, FAKE, 33, 4, 144, FAKE, F32, 0, None, BIG, None) == WORKSPACE
+    assert lin(FAKE, F32, FAKE, FAKE, 33, 4, 144, FAKE, F32, 0, MISALIGNED, BIG, None) == ALIGNMENT
+    assert lin(MISALIGNED, F32, FAKE, FAKE, 33, 4, 144, FAKE, F32, 0, FAKE, BIG, None) == ALIGNMENT
+    assert lin(FAKE, F32, FAKE, None, 33, 4, 144, FAKE, F32, 0, FAKE, BIG, None) == INVALID
+    assert lin(FAKE, F32, FAKE, FAKE, 33, 4, 144, FAKE, F16, 1, FAKE, BIG, None) == UNSUPPORTED
     assert lin(None, F32, None, None, 0, 4, 144, None, F32, 0, None, 0, None) == OK
 
 

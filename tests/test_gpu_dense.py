@@ -484,7 +484,7 @@ def test_wrappers_refuse_mismatched_tensors(api):
     with pytest.raises(api.TQError, match="UNSUPPORTED"):
         api.fp8_block_linear(x, w, s_w, out=torch.zeros(4, 130, dtype=BF16, device="cuda"), accumulate=True)
     with pytest.raises(api.TQError, match="WORKSPACE"):
-        api.fp8_block_linear(x, w, s_w, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        api.fp8_block_linear(rand((40, 64), 1), w, s_w, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError, match="block_rows"):
         api.fp8_block_quantize(x, 64)
 

@@ -89,7 +89,7 @@ SIGNATURES = {
     "fp8_block_quantize": ([_VP, _I, _I64, _I, _I, _VP, _VP, _VP], _I),
     "fp8_block_dequantize": ([_VP, _VP, _I64, _I, _I, _VP, _I, _VP], _I),
     "fp8_block_gemm": ([_VP, _VP, _VP, _VP, _I, _I, _I, _VP, _I, _I, _VP], _I),
-    "fp8_block_linear_workspace_size": ([_I, _I], _SZ),
+    "fp8_block_linear_workspace_size": ([_I, _I, _I], _SZ),
     "fp8_block_linear": ([_VP, _I, _VP, _VP, _I, _I, _I, _VP, _I, _I, _VP, _SZ, _VP], _I),
     "swiglu_forward": ([_VP, _VP, _VP, _I, _I, _I, _I, _VP, ctypes.POINTER(TqSwigluSaved), _VP], _I),
     "swiglu_backward_workspace_size": ([_I, _I, _I, _I], _SZ),
@@ -538,8 +538,8 @@ def fp8_block_gemm(x: torch.Tensor, s_x: torch.Tensor, w: torch.Tensor, s_w: tor
     return out
 
 
-def fp8_block_linear_workspace_size(M: int, K: int) -> int:
-    return int(_fn("fp8_block_linear_workspace_size")(M, K))
+def fp8_block_linear_workspace_size(M: int, N: int, K: int) -> int:
+    return int(_fn("fp8_block_linear_workspace_size")(M, N, K))
 
 
 def fp8_block_linear(x: torch.Tensor, w: torch.Tensor, s_w: torch.Tensor, out: Optional[torch.Tensor] = None,
@@ -551,10 +551,14 @@ def fp8_block_linear(x: torch.Tensor, w: torch.Tensor, s_w: torch.Tensor, out: O
     M, K, dev = _require_matrix(x, x.dtype, "x")
     N = _fp8_weight(w, s_w, K, dev)
     out = _fp8_out(out, out_dtype, (M, N), dev, accumulate, stream)
-    ws = _workspace(ws, fp8_block_linear_workspace_size(M, K), dev, stream)
+    need = fp8_block_linear_workspace_size(M, N, K)
+    ptr, size = 0, 0
+    if ws is not None or need:
+        ws = _workspace(ws, need, dev, stream)
+        ptr, size = ws.data_ptr(), ws.numel() * ws.element_size()
     _check(_fn("fp8_block_linear")(x.data_ptr(), dt, w.data_ptr(), s_w.data_ptr(), M, N, K, out.data_ptr(),
-                                   TQ_DTYPE[out.dtype], int(accumulate), ws.data_ptr(),
-                                   ws.numel() * ws.element_size(), _raw_stream(stream, dev)), "fp8_block_linear")
+                                   TQ_DTYPE[out.dtype], int(accumulate), ptr, size, _raw_stream(stream, dev)),
+           "fp8_block_linear")
     return out
 
 
@@ -805,7 +809,7 @@ class MoeBuffers:
         self.shared_h = self.shared_ws = None
         if shared is not None:
             self.shared_h = torch.empty((T, shared.F), dtype=shared.w_gate.dtype, device=dev)
-            self.shared_ws = torch.empty(max(fp8_block_linear_workspace_size(T, shared.F), 16), dtype=torch.uint8,
+            self.shared_ws = torch.empty(max(fp8_block_linear_workspace_size(T, layer.D, shared.F), 16), dtype=torch.uint8,
                                          device=dev)
 
 

@@ -13,34 +13,53 @@
 //   kFp8:    a K-block is one 128-wide scale block; its 128 x N product (exact E4M3
 //            products, fp32 sums in tensor memory) is scaled by s_w * s_x[t] and added
 //            to fp32 registers.
+//   kFp8Store: kFp8 from 16- or 32-bit activations of up to 16 tokens: six warps store the
+//            CTA's share of the token rows as E4M3 blocks in shared memory (as
+//            fp8_block_quantize does) while the first weights are on their way, so there is
+//            no launch before this one and no workspace.
 #pragma once
 
 #include "tq_dense.cuh"
+#include "tq_fp8_store.cuh"
 
 namespace tq {
 
-constexpr int kSwiglu = 0, kFp8 = 1;
+constexpr int kSwiglu = 0, kFp8 = 1, kFp8Store = 2;
 constexpr int kRowsM = 128;
 constexpr int kRowsThreads = 256;   // warp 0 TMA, 1 MMA, 2 TMEM, 4-7 accumulators; all add partial sums
 
+// kFp8Store: the CTA's K-blocks whose stored tokens fit next to the ring, two CTAs a SM.
+template <int N>
+struct RowsStore {
+    static constexpr int kBlockBytes = N * 128 + N * 4;      // E4M3 rows and their scales
+    static constexpr int kMost = (46 * 1024) / kBlockBytes;  // 22 for N = 16
+};
+constexpr int kMostStored = 22;
+
 template <int N, int KIND>
 struct RowsShape {
-    static constexpr int kStageBytes = kRowsM * 128 + N * 128;
-    static constexpr int kStages = (104 * 1024) / kStageBytes < 6 ? (104 * 1024) / kStageBytes : 6;
-    static constexpr int kAccStages = KIND == kFp8 ? (N <= 64 ? 4 : 2) : 1;
+    static constexpr bool kIsFp8 = KIND != kSwiglu;
+    static constexpr int kStageBytes = kRowsM * 128 + (KIND == kFp8Store ? 0 : N * 128);
+    static constexpr int kMostStages = KIND == kFp8Store ? 4 : 6;
+    static constexpr int kStages = (104 * 1024) / kStageBytes < kMostStages ? (104 * 1024) / kStageBytes : kMostStages;
+    static constexpr int kAccStages = kIsFp8 ? (N <= 64 ? 4 : 2) : 1;
     static constexpr int kTmemCols = N * kAccStages < 32 ? 32 : N * kAccStages;
     static constexpr int kRing = kStages * kStageBytes;
     static_assert(kStages >= 2 && kRing >= kRowsM * N * 4, "the ring also holds the partial sums");
-    static constexpr int kBytes = kRing + 1024 + 256 + (KIND == kFp8 ? 4 * kAccStages * N : 0);
+    static constexpr int kStored = KIND == kFp8Store ? RowsStore<N>::kMost * N * 128 : 0;
+    // scales: [acc stage][N] s_x s_w (kFp8), or [K-block][N] s_x (kFp8Store)
+    static constexpr int kScales = KIND == kFp8Store ? RowsStore<N>::kMost * N * 4 : KIND == kFp8 ? 4 * kAccStages * N : 0;
+    static constexpr int kBytes = kRing + kStored + 1024 + 512 + kScales;
 };
 
 struct RowsBars {
     uint64_t full[6], empty[6];
     uint64_t acc_full[4], acc_empty[4];
+    uint64_t stored[kMostStored];     // kFp8Store: the K-block's token rows are in shared memory
     uint32_t tmem_base;
     int32_t abort;
 };
-static_assert(sizeof(RowsBars) <= 256, "barrier block");
+static_assert(sizeof(RowsBars) <= 512 && RowsStore<16>::kMost <= kMostStored, "barrier block");
 
 struct RowsArgs {
     int rows;             // tokens
@@ -49,7 +68,9 @@ struct RowsArgs {
     int out_type;         // tq_dtype
     int accumulate;       // kFp8 with fp32 output: y += ...
     void *out;
-    const float *sx;      // [rows][kblocks]
+    const float *sx;      // [rows][kblocks] (kFp8)
+    const void *x;        // [rows][cols] of x_type (kFp8Store)
+    int cols, x_type;
     const float *sw;      // [ceil(width / 128)][kblocks]
 };
 
@@ -81,29 +102,71 @@ __device__ __forceinline__ void store_out4(void *out, size_t i, const float (&v)
     }
 }
 
+// Storing warp w of 6: every sixth K-block of the CTA's token rows as E4M3 in the 128-byte
+// swizzle the MMA reads, 16 lanes a row and 8 rows in flight.  Rows past the last token are
+// left as they are: a product's columns do not mix, and theirs are not stored.
+template <typename T, int N>
+__device__ __forceinline__ void rows_store(const RowsArgs &args, unsigned char *tokens, float *scales, uint64_t *stored,
+                                           int t0, int kb0, int nkb, int w, int lane) {
+    const int half = lane >> 4, sub = lane & 15;
+    const int rows = min(N, args.rows - t0);
+    const T *x = reinterpret_cast<const T *>(args.x) + (size_t)t0 * args.cols;
+    for (int i = w; i < nkb; i += 6) {
+        const int c = (kb0 + i) * 128 + sub * 8;
+        unsigned char *dst = tokens + i * (N * 128);
+#pragma unroll 1
+        for (int r0 = 0; r0 < rows; r0 += 16) {
+            float v[8][8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int r = r0 + 2 * k + half;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) v[k][j] = 0.f;
+                if (r < rows && c < args.cols) load8<T>(x + (size_t)r * args.cols + c, v[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (r0 + 2 * k >= rows) break;
+                const int r = r0 + 2 * k + half;
+                float scale;
+                const uint2 q = fp8_store_block(v[k], scale);
+                // 16-byte chunk (sub / 2) of row r lies at chunk (sub / 2) ^ (r mod 8)
+                *reinterpret_cast<uint2 *>(dst + r * 128 + (((sub >> 1) ^ (r & 7)) << 4) + (sub & 1) * 8) = q;
+                if (sub == 0) scales[i * N + r] = scale;
+            }
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&stored[i]);
+    }
+}
+
 template <int N, int KIND>
-__global__ void __launch_bounds__(kRowsThreads, KIND == kFp8 && N > 64 ? 1 : 2)
+__global__ void __launch_bounds__(kRowsThreads, KIND != kSwiglu && N > 64 ? 1 : 2)
     dense_rows_kernel(const __grid_constant__ CUtensorMap map_w0, const __grid_constant__ CUtensorMap map_w1,
                       const __grid_constant__ CUtensorMap map_x, const RowsArgs args) {
     using SH = RowsShape<N, KIND>;
     extern __shared__ __align__(128) unsigned char smem_raw[];
     const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
     unsigned char *ring = smem_raw + pad;
-    RowsBars &sm = *reinterpret_cast<RowsBars *>(ring + SH::kRing);
-    float *scales = reinterpret_cast<float *>(ring + SH::kRing + 256);   // [acc stage][N], kFp8 only
+    unsigned char *tokens = ring + SH::kRing;                            // kFp8Store: [K-block][N][128]
+    RowsBars &sm = *reinterpret_cast<RowsBars *>(tokens + SH::kStored);
+    float *scales = reinterpret_cast<float *>(tokens + SH::kStored + 512);   // E4M3 only
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int C = (int)cluster_size(), rank = (int)cluster_rank();
     const int tile = blockIdx.x / C;
     const int t0 = blockIdx.y * N;
     const int kb0 = (int)((long long)args.kblocks * rank / C);
     const int nkb = (int)((long long)args.kblocks * (rank + 1) / C) - kb0;
-    const int cols_per_kb = KIND == kFp8 ? 128 : 64;
+    const int cols_per_kb = SH::kIsFp8 ? 128 : 64;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < SH::kStages; ++i) {
             mbar_init(&sm.full[i], 1);
             mbar_init(&sm.empty[i], 1);
         }
+        if (KIND == kFp8Store)
+            for (int i = 0; i < RowsStore<N>::kMost; ++i) mbar_init(&sm.stored[i], 1);
         for (int i = 0; i < SH::kAccStages; ++i) {
             mbar_init(&sm.acc_full[i], 1);
             mbar_init(&sm.acc_empty[i], 4);
@@ -126,6 +189,17 @@ __global__ void __launch_bounds__(kRowsThreads, KIND == kFp8 && N > 64 ? 1 : 2)
         return ok;
     };
 
+    if constexpr (KIND == kFp8Store) {
+        // warps 2-7; 4-7 then go on to accumulate
+        if (warp >= 2) {
+            if (args.x_type == TQ_DTYPE_F32)
+                rows_store<float, N>(args, tokens, scales, sm.stored, t0, kb0, nkb, warp - 2, lane);
+            else if (args.x_type == TQ_DTYPE_F16)
+                rows_store<__half, N>(args, tokens, scales, sm.stored, t0, kb0, nkb, warp - 2, lane);
+            else
+                rows_store<__nv_bfloat16, N>(args, tokens, scales, sm.stored, t0, kb0, nkb, warp - 2, lane);
+        }
+    }
     if (warp == 0) {
         if (lane == 0) {
             int issued = 0;
@@ -141,7 +215,7 @@ __global__ void __launch_bounds__(kRowsThreads, KIND == kFp8 && N > 64 ? 1 : 2)
                 } else {
                     tma_load_2d(a, &map_w0, x, tile * kRowsM, &sm.full[s]);
                 }
-                tma_load_2d(a + kRowsM * 128, &map_x, x, t0, &sm.full[s]);
+                if (KIND != kFp8Store) tma_load_2d(a + kRowsM * 128, &map_x, x, t0, &sm.full[s]);
                 ++issued;
             }
             // every issued copy has landed before the ring is used for anything else
@@ -150,21 +224,23 @@ __global__ void __launch_bounds__(kRowsThreads, KIND == kFp8 && N > 64 ? 1 : 2)
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            const uint32_t idesc = umma_idesc(kRowsM, N, KIND == kFp8 ? 0 : (args.out_type == TQ_DTYPE_BF16 ? 1 : 0), 0, 0);
+            const uint32_t idesc = umma_idesc(kRowsM, N, SH::kIsFp8 ? 0 : (args.out_type == TQ_DTYPE_BF16 ? 1 : 0), 0, 0);
             for (int i = 0; i < nkb; ++i) {
                 const int s = i % SH::kStages, st = i % SH::kAccStages;
                 if (!wait(&sm.full[s], (i / SH::kStages) & 1)) break;
-                if (KIND == kFp8 && i >= SH::kAccStages && !wait(&sm.acc_empty[st], (i / SH::kAccStages - 1) & 1)) break;
+                if (KIND == kFp8Store && !wait(&sm.stored[i], 0)) break;
+                if (SH::kIsFp8 && i >= SH::kAccStages && !wait(&sm.acc_empty[st], (i / SH::kAccStages - 1) & 1)) break;
                 tc_fence_after();
                 const uint32_t base = smem_u32(ring + s * SH::kStageBytes);
-                const uint64_t ad = umma_desc_sw128(base), bd = umma_desc_sw128(base + kRowsM * 128);
+                const uint64_t ad = umma_desc_sw128(base), bd = umma_desc_sw128(
+                    KIND == kFp8Store ? smem_u32(tokens + i * (N * 128)) : base + kRowsM * 128);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    if (KIND == kFp8) umma_e4m3(tmem + st * N, ad + 2 * k, bd + 2 * k, idesc, k != 0);
+                    if (SH::kIsFp8) umma_e4m3(tmem + st * N, ad + 2 * k, bd + 2 * k, idesc, k != 0);
                     else umma_f16(tmem, ad + 2 * k, bd + 2 * k, idesc, (i | k) != 0);
                 }
                 umma_commit(&sm.empty[s]);
-                if (KIND == kFp8) umma_commit(&sm.acc_full[st]);
+                if (SH::kIsFp8) umma_commit(&sm.acc_full[st]);
             }
             if (KIND == kSwiglu) umma_commit(&sm.acc_full[0]);
         }
@@ -192,25 +268,35 @@ __global__ void __launch_bounds__(kRowsThreads, KIND == kFp8 && N > 64 ? 1 : 2)
             const bool mine = et < N && t0 + et < args.rows;
             const float *sx = args.sx + (size_t)(mine ? t0 + et : 0) * args.kblocks + kb0;
             const float *sw = args.sw + (size_t)tile * args.kblocks + kb0;
-            float next = nkb > 0 ? (mine ? sx[0] : 0.f) * sw[0] : 0.f;
+            float next = 0.f;
+            if (nkb > 0) next = KIND == kFp8Store ? sw[0] : (mine ? sx[0] : 0.f) * sw[0];
             for (int i = 0; i < nkb; ++i) {
                 const int st = i % SH::kAccStages;
-                // the scales of this block; the slot's last readers are past the barrier
-                // of block i - 1
-                if (et < N) scales[st * N + et] = next;
-                if (i + 1 < nkb) next = (mine ? sx[i + 1] : 0.f) * sw[i + 1];
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                const bool ok = wait(&sm.acc_full[st], (i / SH::kAccStages) & 1);
+                const float w = next;
+                const float *slot = scales + (KIND == kFp8Store ? i : st) * N;
+                if constexpr (KIND == kFp8Store) {
+                    if (i + 1 < nkb) next = sw[i + 1];
+                } else {
+                    // the scales of this block; the slot's last readers are past the barrier
+                    // of block i - 1
+                    if (et < N) scales[st * N + et] = w;
+                    if (i + 1 < nkb) next = (mine ? sx[i + 1] : 0.f) * sw[i + 1];
+                    asm volatile("bar.sync 1, 128;" ::: "memory");
+                }
+                const bool ok = __all_sync(0xffffffffu, wait(&sm.acc_full[st], (i / SH::kAccStages) & 1));
                 if (ok) {
                     tc_fence_after();
 #pragma unroll
                     for (int c0 = 0; c0 < N; c0 += 16) {
                         uint32_t v[16];
                         tmem_ld16(taddr + st * N + c0, v);
-                        const float4 *sc = reinterpret_cast<const float4 *>(scales + st * N + c0);
+                        const float4 *sc = reinterpret_cast<const float4 *>(slot + c0);
 #pragma unroll
                         for (int c = 0; c < 16; c += 4) {
-                            const float4 f = sc[c >> 2];
+                            float4 f = sc[c >> 2];
+                            if (KIND == kFp8Store) {
+                                f.x *= w; f.y *= w; f.z *= w; f.w *= w;
+                            }
                             acc[c0 + c] = fmaf(f.x, __uint_as_float(v[c]), acc[c0 + c]);
                             acc[c0 + c + 1] = fmaf(f.y, __uint_as_float(v[c + 1]), acc[c0 + c + 1]);
                             acc[c0 + c + 2] = fmaf(f.z, __uint_as_float(v[c + 2]), acc[c0 + c + 2]);
@@ -265,12 +351,24 @@ __global__ void __launch_bounds__(kRowsThreads, KIND == kFp8 && N > 64 ? 1 : 2)
     cluster_sync_all();                       // no CTA leaves while another reads its ring
 }
 
-// Cluster size of the K split: the most CTAs (up to 8 a tile) that two resident CTAs a SM
-// still take in one wave, with at least two K-blocks each.
-inline int rows_cluster(long long tiles, int kblocks, int n_tokens) {
-    int c = 8;
-    while (c > 1 && (tiles * c > 2LL * num_sms() || 2 * c > kblocks || n_tokens % c)) c >>= 1;
+// Cluster size of the K split: the most CTAs a tile that leave every SM one CTA, or two
+// where only two are to be had by it (and both fit).  More CTAs than that cost more in
+// partial sums than they bring: 203 tokens, 2056 -> 1000, C = 4 (128 CTAs) 8.7 us, C = 8
+// 12.6; 16 tokens, 4096 -> 16384 in E4M3, C = 1, 2, 4: 14.3, 10.9, 14.5.  A SwiGLU tile of 128
+// tokens has 64 KB of partial sums a CTA: 4 CTAs 9.5 us, 8 CTAs 11.1 (128 tokens, 4096 -> 1024).
+template <int N, int KIND>
+inline int rows_cluster(long long tiles, int kblocks) {
+    const bool two = KIND == kSwiglu || N <= 64;
+    int c = KIND == kSwiglu && N > 64 ? 4 : 8;
+    while (c > 1 && (tiles * c > (c == 2 && two ? 2LL : 1LL) * num_sms() || c > kblocks)) c >>= 1;
     return c;
+}
+
+// K-blocks of a CTA with one token tile of N rows.
+template <int N>
+inline int rows_share(int width, int kblocks) {
+    const int c = rows_cluster<N, kFp8Store>((width + (long long)kRowsM - 1) / kRowsM, kblocks);
+    return (kblocks + c - 1) / c;
 }
 
 template <int N, int KIND>
@@ -287,7 +385,7 @@ static int launch_rows(const CUtensorMap &w0, const CUtensorMap &w1, const CUten
     const int per_tile = KIND == kSwiglu ? 64 : kRowsM;
     const long long row_tiles = (a.width + (long long)per_tile - 1) / per_tile;
     const int token_tiles = (a.rows + N - 1) / N;
-    const int c = rows_cluster(row_tiles * token_tiles, a.kblocks, N);
+    const int c = rows_cluster<N, KIND>(row_tiles * token_tiles, a.kblocks);
     cudaError_t e = launch_cluster(dense_rows_kernel<N, KIND>, dim3((unsigned)(row_tiles * c), token_tiles),
                                    dim3(kRowsThreads), SH::kBytes, s, c, chained, w0, w1, x, a);
     return e == cudaSuccess ? launch_status() : record_cuda_error("dense_rows_kernel");

@@ -20,26 +20,6 @@ namespace tq {
 
 // ------------------------------------------------------------------------------ storage
 
-template <typename T>
-__device__ __forceinline__ void load8(const T *p, float (&v)[8]) {
-    if constexpr (sizeof(T) == 4) {
-        const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-        const uint4 a = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float2 f;
-            if constexpr (std::is_same<T, __half>::value) f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-            else f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[i]));
-            v[2 * i] = f.x;
-            v[2 * i + 1] = f.y;
-        }
-    }
-}
-
 // Row kernels: a warp takes kStoreRows rows of 512 columns (4 blocks), 16 lanes a block,
 // 8 values a lane; blockIdx.y is the group of 512 columns, so no index is divided.  All
 // loads of a warp are in flight together (4 a lane), which the reads from HBM need.
@@ -73,18 +53,11 @@ __global__ void __launch_bounds__(kStoreWarps * 32) fp8_quantize_rows_kernel(con
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int c = c0 + 256 * h;
-            const float *w = v[k][h];
-            float m = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) m = finite_max(m, w[j]);
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const int e = e4m3_block_exponent(m);
-            const float inv = exp2_int(-e);
+            float s;
+            const uint2 q = fp8_store_block(v[k][h], s);
             if (r0 + k < rows && c < cols) {
-                *reinterpret_cast<uint2 *>(out + (size_t)(r0 + k) * cols + c) =
-                    make_uint2(e4m3x4_scaled(w[0], w[1], w[2], w[3], inv), e4m3x4_scaled(w[4], w[5], w[6], w[7], inv));
-                if ((lane & 15) == 0) scales[(size_t)(r0 + k) * nb + c / 128] = exp2_int(e);
+                *reinterpret_cast<uint2 *>(out + (size_t)(r0 + k) * cols + c) = q;
+                if ((lane & 15) == 0) scales[(size_t)(r0 + k) * nb + c / 128] = s;
             }
         }
 }
@@ -389,8 +362,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kFp8Threads, 1)
 
 // ------------------------------------------------------------------------------ host side
 
-// Up to this many rows the weight-streaming kernel runs.
-constexpr int kFp8RowsMost = 128;
+// Rows the weight-streaming kernel takes: up to 128 (it is bound by reading w), and as many
+// more as leave a cluster of two CTAs a tile of 128 rows by 128 outputs, one CTA a SM: a pair
+// of the other kernel then has too few tiles (333 x 1001 x 2064: 8.4 us here, 13.2 there; 333 x
+// 4096 x 4096, 96 tiles: 21.9 here, 20.9 there).
+static bool fp8_rows_case(int M, int N) {
+    if (M <= 128) return true;
+    return 2 * ((M + 127LL) / 128) * ((N + 127LL) / 128) <= num_sms();
+}
+
+// Whether the product stores its activations itself (one launch, no workspace): every CTA
+// then stores its share of K for all tokens, which pays up to 128 blocks of a row (1 x 4096 x
+// 4096: 8 blocks, 6.4 us against 7.4 in two launches; 16 x 4096 x 4096: 128 blocks, 8.3 against
+// 8.4; 16 x 16384 x 4096: 256 blocks, 21.6 against 16.6).
+static bool fp8_fused_case(int M, int N, int K) {
+    if (M > 16) return false;
+    const int share = rows_share<16>(N, (K + 127) / 128);
+    return share <= RowsStore<16>::kMost && M * share <= 128;
+}
 
 static int fp8_product(const uint8_t *x8, const float *sx, const uint8_t *w8, const float *sw, int M, int N, int K,
                        void *y, int y_dtype, int accumulate, cudaStream_t s) {
@@ -407,7 +396,7 @@ static int fp8_product(const uint8_t *x8, const float *sx, const uint8_t *w8, co
     const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     int st = matrix_map(&mw, u8, 1, w8, N, K, 128);
     if (st) return st;
-    if (M <= kFp8RowsMost) {
+    if (fp8_rows_case(M, N)) {
         const int n = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
         st = matrix_map(&mx, u8, 1, x8, M, K, n);
         if (st) return st;
@@ -434,6 +423,27 @@ static int fp8_product(const uint8_t *x8, const float *sx, const uint8_t *w8, co
                        mx, mw, a) != cudaSuccess)
         return record_cuda_error("fp8_pair_kernel");
     return launch_status();
+}
+
+// The product of few rows from activations of 16 or 32 bits, one launch.
+static int fp8_product_fused(const void *x, int x_dtype, const uint8_t *w8, const float *sw, int M, int N, int K,
+                             void *y, int y_dtype, int accumulate, cudaStream_t s) {
+    RowsArgs a{};
+    a.rows = M;
+    a.width = N;
+    a.kblocks = (K + 127) / 128;
+    a.out_type = y_dtype;
+    a.accumulate = accumulate;
+    a.out = y;
+    a.sw = sw;
+    a.x = x;
+    a.cols = K;
+    a.x_type = x_dtype;
+    CUtensorMap mw;
+    const int st = matrix_map(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w8, N, K, 128);
+    if (st) return st;
+    LaunchScope ls(s, kStageFp8Gemm);
+    return launch_rows<16, kFp8Store>(mw, mw, mw, a, s, true);
 }
 
 // Shape and type checks of a product; 0 rows or outputs is a valid no-op.
@@ -514,8 +524,8 @@ TQ_API int fp8_block_gemm(const uint8_t *x, const float *s_x, const uint8_t *w, 
     return fp8_product(x, s_x, w, s_w, M, N, K, y, y_dtype, accumulate, (cudaStream_t)stream);
 }
 
-TQ_API size_t fp8_block_linear_workspace_size(int M, int K) {
-    if (M < 0 || K < 1 || K % 16) return 0;
+TQ_API size_t fp8_block_linear_workspace_size(int M, int N, int K) {
+    if (M < 0 || N < 0 || K < 1 || K % 16 || tq::fp8_fused_case(M, N, K)) return 0;
     const size_t q = ((size_t)M * K + 255) & ~(size_t)255;
     return q + (((size_t)M * ((K + 127) / 128) * 4 + 255) & ~(size_t)255);
 }
@@ -529,7 +539,9 @@ TQ_API int fp8_block_linear(const void *x, int x_dtype, const uint8_t *w, const 
     if (!x || !w || !s_w || !y) return TQ_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned16(w) || !aligned16(y) || !aligned16(s_w) || (ws && !aligned16(ws)))
         return TQ_ERR_ALIGNMENT;
-    if (!ws || ws_bytes < fp8_block_linear_workspace_size(M, K)) return TQ_ERR_WORKSPACE;
+    if (fp8_fused_case(M, N, K))
+        return fp8_product_fused(x, x_dtype, w, s_w, M, N, K, y, y_dtype, accumulate, (cudaStream_t)stream);
+    if (!ws || ws_bytes < fp8_block_linear_workspace_size(M, N, K)) return TQ_ERR_WORKSPACE;
     uint8_t *q = reinterpret_cast<uint8_t *>(ws);
     float *sx = reinterpret_cast<float *>(q + (((size_t)M * K + 255) & ~(size_t)255));
     st = fp8_block_quantize(x, x_dtype, M, K, 1, q, sx, stream);

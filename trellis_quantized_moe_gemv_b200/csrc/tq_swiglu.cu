@@ -445,8 +445,13 @@ static bool saved_aligned(const tq_swiglu_saved *s) {
            aligned16(s->s_u);
 }
 
-// Up to this many tokens the weight-streaming kernel runs (tokens on the MMA's N side).
-constexpr int kSwigluRowsMost = 128;
+// Tokens the weight-streaming kernel takes: up to 128 (it is bound by reading the weights), and
+// as many more as leave two CTAs a tile of 128 tokens by 64 outputs, two CTAs a SM: the pair
+// kernel then has too few tiles (203 tokens, 2056 -> 1000: 8.7 us here, 14.3 there; 1024 tokens,
+// 4096 -> 1024: 19.4 here, 24.4 there; 2048 tokens: 31.8 here, 26.3 there).
+static bool swiglu_rows_case(int T, int F) {
+    return T <= 128 || ((T + 127LL) / 128) * ((F + 63LL) / 64) <= num_sms();
+}
 
 static int swiglu_rows(const void *x, const void *wg, const void *wu, int f16, int T, int D, int F, void *h,
                        cudaStream_t s) {
@@ -487,7 +492,7 @@ TQ_API int swiglu_forward(const void *x, const void *w_gate, const void *w_up, i
         return TQ_ERR_ALIGNMENT;
     const cudaStream_t s = (cudaStream_t)stream;
     const int f16 = dtype == TQ_DTYPE_F16;
-    if (!saved && T <= kSwigluRowsMost) return swiglu_rows(x, w_gate, w_up, f16, T, D, F, h, s);
+    if (!saved && swiglu_rows_case(T, F)) return swiglu_rows(x, w_gate, w_up, f16, T, D, F, h, s);
     if (saved) {
         st = fp8_block_quantize(x, dtype, T, D, 1, saved->x, saved->s_x, stream);
         if (st) return st;
