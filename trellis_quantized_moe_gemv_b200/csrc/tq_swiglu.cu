@@ -59,51 +59,63 @@ struct PairArgs {
     const __nv_bfloat16 *dh;                  // [T][F]
     __nv_bfloat16 *dg, *du;                   // [T][F]
     __nv_bfloat16 *dx, *dwg, *dwu;            // [T][D], [F][D], [F][D]
+    // tile plan (plan_gateup, plan_grads)
+    long long full;                           // gate/up: whole tiles; the others are halved
+    long long tiles;                          // gate/up: tiles, halves counted one by one
+    int halved;                               // gradients: every tile is half as wide
+    long long n_dw, n_dx;                     // gradients: tiles of each kind
+    int more;                                 // gradients: pairs that have one dw tile more than the rest,
+    long long dx_more, dx_rest;               //   and the dx tiles of such a pair and of another
 };
 
 enum PairKind { kPairForward = 0, kPairSave = 1, kPairRecompute = 2, kPairGrads = 3 };
 
-// One output tile: rows m0 .. m0 + 255 of the pair, columns n0 .. n0 + 255 (gate/up: 128
-// outputs), `which` the matrix of a weight gradient (0 gate, 1 up; -1 dx).
+// One output tile: rows m0 .. m0 + 255 of the pair, columns n0 .. n0 + width - 1 (gate/up:
+// width / 2 outputs; width 256, or 128 for a halved tile), `which` the matrix of a weight
+// gradient (0 gate, 1 up; -1 dx).
 struct PairTile {
-    int m0, n0, kblocks, which;
+    int m0, n0, width, kblocks, which;
 };
 
+// The j-th tile of a pair; false past its last.
 template <int KIND>
-__device__ __forceinline__ long long pair_tiles(const PairArgs &p) {
-    const long long mt = (p.T + kPairM - 1) / kPairM;
-    if (KIND != kPairGrads) return mt * ((p.F + 127) / 128);
-    const long long nd = (p.D + kPairN - 1) / kPairN;
-    return (2LL * ((p.F + kPairM - 1) / kPairM) + mt) * nd;
-}
-
-template <int KIND>
-__device__ __forceinline__ PairTile pair_tile(const PairArgs &p, long long t) {
-    PairTile r;
+__device__ __forceinline__ bool pair_tile(const PairArgs &p, long long pair, long long pairs, long long j, PairTile &r) {
     int m, n;
     if (KIND != kPairGrads) {
+        // whole tiles first, then the halves of the last ones
+        long long t = pair + j * pairs;
+        if (t >= p.tiles) return false;
+        const bool half = t >= p.full;
+        const int part = half ? (int)((t - p.full) & 1) : 0;
+        if (half) t = p.full + ((t - p.full) >> 1);
         grouped_tile(t, (p.T + kPairM - 1) / kPairM, (p.F + 127) / 128, m, n);
         r.m0 = m * kPairM;
-        r.n0 = n * 128;
+        r.n0 = n * 128 + 64 * part;
+        r.width = half ? 128 : 256;
         r.kblocks = (p.D + 63) / 64;
         r.which = -1;
-        return r;
+        return true;
     }
-    const int nd = (p.D + kPairN - 1) / kPairN, mf = (p.F + kPairM - 1) / kPairM;
-    const long long dw = 2LL * mf * nd;
-    if (t < dw) {
-        grouped_tile(t, 2 * mf, nd, m, n);
+    r.width = p.halved ? 128 : 256;
+    const int nd = (p.D + r.width - 1) / r.width, mf = (p.F + kPairM - 1) / kPairM;
+    const bool more = pair < p.more;
+    const long long dw = p.n_dw / pairs + (more ? 1 : 0);
+    if (j < dw) {
+        grouped_tile(pair + j * pairs, 2 * mf, nd, m, n);
         r.which = m >= mf;
         r.m0 = (m - (r.which ? mf : 0)) * kPairM;
         r.kblocks = (p.T + 63) / 64;
     } else {
-        grouped_tile(t - dw, (p.T + kPairM - 1) / kPairM, nd, m, n);
+        const long long k = j - dw, split = p.more * p.dx_more;
+        const long long t = more ? pair + k * p.more : split + (pair - p.more) + k * (pairs - p.more);
+        if (k >= (more ? p.dx_more : p.dx_rest) || t >= p.n_dx) return false;
+        grouped_tile(t, (p.T + kPairM - 1) / kPairM, nd, m, n);
         r.which = -1;
         r.m0 = m * kPairM;
         r.kblocks = 2 * ((p.F + 63) / 64);
     }
-    r.n0 = n * kPairN;
-    return r;
+    r.n0 = n * r.width;
+    return true;
 }
 
 // ------------------------------------------------------------------------------ epilogues
@@ -128,8 +140,9 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs &p, const PairTile 
     if constexpr (KIND == kPairGrads) {
         __nv_bfloat16 *out = t.which < 0 ? p.dx : (t.which ? p.dwu : p.dwg);
         const int rows = (t.which < 0 ? p.T : p.F) - r0;
+        const int cols = t.width / 2;
 #pragma unroll 1
-        for (int c = 128 * w; c < 128 * w + 128; c += 64) {
+        for (int c = cols * w; c < cols * w + cols; c += 64) {
             tmem_ld32(taddr + c, a);
             tmem_ld32(taddr + c + 32, b);
             tmem_ld_wait();
@@ -182,11 +195,15 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs &p, const PairTile 
                            (size_t)p.F, rows, p.F - t.n0, p.F % 16 == 0);
     }
     uint4 o2[8];     // du (backward)
+    // the warp's columns: 64, or 32 of a halved tile (the second half of o is then not stored)
+    const bool halved = t.width != 256;
+    const int c0 = (halved ? 32 : 64) * w, u0 = t.width / 2;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-        const int c = 64 * w + 32 * half;
+        if (half && halved) break;
+        const int c = c0 + 32 * half;
         tmem_ld32(taddr + c, a);
-        tmem_ld32(taddr + 128 + c, b);
+        tmem_ld32(taddr + u0 + c, b);
         const int col = t.n0 + c;
         if constexpr (KIND == kPairRecompute) {
             uint4 d[4];
@@ -212,16 +229,14 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs &p, const PairTile 
             pack_row32(v, p.f16 != 0, o + 4 * half);
         }
     }
-    const int col = t.n0 + 64 * w;
+    const int col = t.n0 + c0;
+    const int bytes = min((p.F - col) * 2, halved ? 64 : 128);
     const size_t at = (size_t)r0 * p.F + col;
     if constexpr (KIND == kPairRecompute) {
-        warp_store_rows<2>(stage, lane, o, reinterpret_cast<char *>(p.dg + at), (size_t)p.F * 2, rows, (p.F - col) * 2,
-                           true);
-        warp_store_rows<2>(stage, lane, o2, reinterpret_cast<char *>(p.du + at), (size_t)p.F * 2, rows, (p.F - col) * 2,
-                           true);
+        warp_store_rows<2>(stage, lane, o, reinterpret_cast<char *>(p.dg + at), (size_t)p.F * 2, rows, bytes, true);
+        warp_store_rows<2>(stage, lane, o2, reinterpret_cast<char *>(p.du + at), (size_t)p.F * 2, rows, bytes, true);
     } else {
-        warp_store_rows<2>(stage, lane, o, reinterpret_cast<char *>(p.h) + at * 2, (size_t)p.F * 2, rows,
-                           (p.F - col) * 2, true);
+        warp_store_rows<2>(stage, lane, o, reinterpret_cast<char *>(p.h) + at * 2, (size_t)p.F * 2, rows, bytes, true);
     }
 }
 
@@ -235,7 +250,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     PairSmem &sm = *reinterpret_cast<PairSmem *>(smem_raw + pad);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank();
-    const long long tiles = pair_tiles<KIND>(args);
     const long long pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
@@ -270,14 +284,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (lane == 0) {
             bool ok = true;
             uint32_t it = 0;
-            // operand tile of 128 rows x 64 K in two 64 x 64 boxes: K-major (rows then K)
+            // operand tile of 64 or 128 rows x 64 K in 64 x 64 boxes: K-major (rows then K)
             // or MN-major (K rows of 64 consecutive matrix columns)
-            auto load = [&](unsigned char *dst, const CUtensorMap *m, int r0, int k0, bool mn, uint32_t bar) {
+            auto load = [&](unsigned char *dst, const CUtensorMap *m, int r0, int k0, bool mn, bool two, uint32_t bar) {
                 tma_load_2d_pair(dst, m, mn ? r0 : k0, mn ? k0 : r0, bar);
-                tma_load_2d_pair(dst + 8192, m, mn ? r0 + 64 : k0, mn ? k0 : r0 + 64, bar);
+                if (two) tma_load_2d_pair(dst + 8192, m, mn ? r0 + 64 : k0, mn ? k0 : r0 + 64, bar);
             };
-            for (long long t = pair; t < tiles && ok; t += pairs) {
-                const PairTile tl = pair_tile<KIND>(args, t);
+            PairTile tl;
+            for (long long j = 0; ok && pair_tile<KIND>(args, pair, pairs, j, tl); ++j) {
+                const bool two = tl.width == 256;         // B rows of a CTA: 128, or 64
+                const int nb = tl.n0 + (tl.width / 2) * rank;
+                const uint32_t bytes = 2 * (kPairStageBytes + (two ? kPairStageBytes : kPairStageBytes / 2));
                 const int half = (args.F + 63) / 64;      // dx: K-blocks of dg, then of du
                 for (int kb = 0; kb < tl.kblocks; ++kb, ++it) {
                     const int s = it % kPairStages;
@@ -286,19 +303,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         break;
                     }
                     const uint32_t bar = map_to_rank(smem_u32(&sm.full[s]), 0);
-                    if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 4 * kPairStageBytes);
+                    if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], bytes);
                     const int ar = tl.m0 + 128 * rank;
                     if (KIND != kPairGrads) {
-                        load(sm.a[s], &maps.a0, ar, kb * 64, false, bar);
-                        load(sm.b[s], rank ? &maps.b1 : &maps.b0, tl.n0, kb * 64, false, bar);
+                        load(sm.a[s], &maps.a0, ar, kb * 64, false, true, bar);
+                        load(sm.b[s], rank ? &maps.b1 : &maps.b0, tl.n0, kb * 64, false, two, bar);
                     } else if (tl.which >= 0) {
-                        load(sm.a[s], tl.which ? &maps.a1 : &maps.a0, ar, kb * 64, true, bar);
-                        load(sm.b[s], &maps.x, tl.n0 + 128 * rank, kb * 64, true, bar);
+                        load(sm.a[s], tl.which ? &maps.a1 : &maps.a0, ar, kb * 64, true, true, bar);
+                        load(sm.b[s], &maps.x, nb, kb * 64, true, two, bar);
                     } else {
                         const bool up = kb >= half;
                         const int k0 = (up ? kb - half : kb) * 64;
-                        load(sm.a[s], up ? &maps.a1 : &maps.a0, ar, k0, false, bar);
-                        load(sm.b[s], up ? &maps.b1 : &maps.b0, tl.n0 + 128 * rank, k0, true, bar);
+                        load(sm.a[s], up ? &maps.a1 : &maps.a0, ar, k0, false, true, bar);
+                        load(sm.b[s], up ? &maps.b1 : &maps.b0, nb, k0, true, two, bar);
                     }
                 }
             }
@@ -312,12 +329,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     } else if (warp == 1) {
         if (rank == 0 && lane == 0) {
             bool ok = true;
-            uint32_t it = 0, j = 0;
+            uint32_t it = 0;
             const int fmt = args.f16 ? 0 : 1;
-            for (long long t = pair; t < tiles && ok; t += pairs, ++j) {
-                const PairTile tl = pair_tile<KIND>(args, t);
+            PairTile tl;
+            for (uint32_t j = 0; ok && pair_tile<KIND>(args, pair, pairs, j, tl); ++j) {
                 const bool a_mn = KIND == kPairGrads && tl.which >= 0, b_mn = KIND == kPairGrads;
-                const uint32_t idesc = umma_idesc(kPairM, kPairN, fmt, a_mn, b_mn);
+                const uint32_t idesc = umma_idesc(kPairM, tl.width, fmt, a_mn, b_mn);
                 const uint32_t st = j & 1, d = tmem + st * kPairN;
                 if (j >= 2 && !wait(&sm.acc_empty[st], ((j >> 1) - 1) & 1)) break;
                 tc_fence_after();
@@ -342,9 +359,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         }
     } else if (warp >= 4) {
         const int q = warp & 3, w = (warp - 4) >> 2;
-        uint32_t j = 0;
-        for (long long t = pair; t < tiles; t += pairs, ++j) {
-            const PairTile tl = pair_tile<KIND>(args, t);
+        PairTile tl;
+        for (uint32_t j = 0; pair_tile<KIND>(args, pair, pairs, j, tl); ++j) {
             const uint32_t st = j & 1;
             const bool ok = __all_sync(0xffffffffu, wait(&sm.acc_full[st], (j >> 1) & 1));
             if (!ok) break;
@@ -410,8 +426,57 @@ static int pair_map(CUtensorMap *m, const void *base, long long rows, long long 
                       64);
 }
 
+// Gate/up tiles: where the last round over the pairs would leave half of them or more without
+// work, its tiles are halved in width (not where they store 8-bit blocks, which need all
+// 128 columns).  8192 tokens, 4096 -> 1024: 256 tiles on 74 pairs are 3 rounds and 34 tiles, or 68
+// halves; %s.
+static long long plan_gateup(PairArgs &p, long long pairs, bool may_halve) {
+    const long long n = (((long long)p.T + kPairM - 1) / kPairM) * ((p.F + 127LL) / 128), last = n % pairs;
+    p.full = may_halve && 2 * last <= pairs ? n - last : n;
+    p.tiles = p.full + 2 * (n - p.full);
+    return p.tiles;
+}
+
+// Gradient tiles: the dw tiles go round the pairs first; the dx tiles then fill up, so that
+// the most loaded pair has least.  All tiles are halved where that ends sooner (few tiles).
+static long long plan_grads(PairArgs &p, long long pairs) {
+    const long long mf = ((long long)p.F + kPairM - 1) / kPairM, mt = ((long long)p.T + kPairM - 1) / kPairM;
+    const long long k_dw = ((long long)p.T + 63) / 64, k_dx = 2 * (((long long)p.F + 63) / 64);
+    double best = 0;
+    for (int halved = 0; halved < 2; ++halved) {
+        const long long width = halved ? 128 : 256, nd = (p.D + width - 1) / width;
+        const long long n_dw = 2 * mf * nd, n_dx = mt * nd;
+        const long long on = n_dw + n_dx < pairs ? n_dw + n_dx : pairs;      // pairs at work
+        const long long q = n_dw / on, more = n_dw % on, rest = on - more;
+        // dx tiles of a pair with q + 1 dw tiles: a, of the others: b
+        long long a = 0, b = 0, load = -1;
+        for (long long x = 0; x <= (more ? (n_dx + more - 1) / more : 0); ++x) {
+            const long long left = n_dx - more * x, y = left > 0 ? (left + rest - 1) / rest : 0;
+            const long long l1 = more ? (q + 1) * k_dw + x * k_dx : 0, l0 = q * k_dw + y * k_dx, l = l1 > l0 ? l1 : l0;
+            if (load < 0 || l < load) {
+                load = l;
+                a = x;
+                b = y;
+            }
+            if (left <= 0) break;
+        }
+        // a halved tile takes a little more than half of a whole one's time: A is read as often
+        const double cost = (double)load * (halved ? 0.6 : 1.0);
+        if (!halved || cost < best) {
+            best = cost;
+            p.halved = halved;
+            p.n_dw = n_dw;
+            p.n_dx = n_dx;
+            p.more = (int)more;
+            p.dx_more = a;
+            p.dx_rest = b;
+        }
+    }
+    return p.n_dw + p.n_dx;
+}
+
 template <int KIND>
-static int launch_pair(const PairMaps &maps, const PairArgs &p, cudaStream_t s, int stage) {
+static int launch_pair(const PairMaps &maps, PairArgs p, cudaStream_t s, int stage) {
     static PerDeviceFlag configured;
     const int smem = (int)sizeof(PairSmem) + 1024;
     if (!configured.get()) {
@@ -420,11 +485,8 @@ static int launch_pair(const PairMaps &maps, const PairArgs &p, cudaStream_t s, 
             return record_cuda_error("cudaFuncSetAttribute(pair_gemm_kernel)");
         configured.set();
     }
-    const long long mt = ((long long)p.T + kPairM - 1) / kPairM;
-    long long tiles = mt * ((p.F + 127LL) / 128);
-    if (KIND == kPairGrads)
-        tiles = (2 * (((long long)p.F + kPairM - 1) / kPairM) + mt) * (((long long)p.D + kPairN - 1) / kPairN);
     const long long pairs = num_sms() / 2;
+    const long long tiles = KIND == kPairGrads ? plan_grads(p, pairs) : plan_gateup(p, pairs, KIND != kPairSave);
     const unsigned grid = 2 * (unsigned)(tiles < pairs ? tiles : pairs);
     LaunchScope ls(s, stage);
     if (launch_chained(pair_gemm_kernel<KIND>, dim3(grid), dim3(kPairThreads), smem, s, maps, p) != cudaSuccess)
