@@ -409,10 +409,16 @@ def _blocks(n: int) -> int:
     return -(-n // BLOCK)
 
 
+def _here() -> int:
+    """The current device, where the kernels run (before CUDA is in use there is none)."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+
+
+# The checks below decide the usual case in one expression and look for the reason only where it
+# fails: they are a good part of a call that takes a few microseconds.
+
 def _require_dense(t, dtype, shape, name, dev):
-    """A contiguous CUDA tensor of this dtype and shape on the current device `dev`, where the
-    kernels run.  One expression decides the usual case: these checks are a good part of a
-    call that takes a few microseconds."""
+    """A contiguous CUDA tensor of this dtype and shape on device `dev`, the current one."""
     if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.get_device() == dev
             and t.shape == shape and t.is_contiguous()):
         return
@@ -422,49 +428,52 @@ def _require_dense(t, dtype, shape, name, dev):
     raise ValueError("%s is on %s, but the current device is cuda:%d" % (name, t.device, dev))
 
 
-def _require_matrix(t, dtype, name):
-    """(rows, columns, current device) of a contiguous matrix on the current device."""
+def _require_matrix(t, dtype, name, dev):
+    """The shape of a contiguous matrix on device `dev`, the current one."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.get_device() == dev
+            and t.dim() == 2 and t.is_contiguous()):
+        return t.shape
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.dim() != 2:
         raise ValueError("%s must be a matrix, got %d dimensions" % (name, t.dim()))
-    if not t.is_cuda:
-        _require(t, dtype, name)
-    dev = torch.cuda.current_device()
-    _require_dense(t, dtype, t.shape, name, dev)
-    return t.shape[0], t.shape[1], dev
+    _require(t, dtype, name)
+    raise ValueError("%s is on %s, but the current device is cuda:%d" % (name, t.device, dev))
 
 
 def _raw_stream(stream, dev):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _new(shape, dtype, dev, stream):
-    """An uninitialised tensor for a call on `stream` (None: the current stream).  Memory for
+def _new(rows, cols, dtype, device, stream):
+    """An uninitialised matrix for a call on `stream` (None: the current stream).  Memory for
     another stream comes from that stream's pool, so that nothing still running on the
     current stream owns it, and is kept until the current stream's uses of it are over."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(rows, cols, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=dev)
+        t = torch.empty(rows, cols, dtype=dtype, device=device)
     t.record_stream(torch.cuda.current_stream())
     return t
 
 
-def _out(out, shape, dtype, name, dev, stream):
+def _out(out, rows, cols, dtype, name, like, dev, stream):
     if out is None:
-        return _new(shape, dtype, dev, stream)
-    _require_dense(out, dtype, shape, name, dev)
+        return _new(rows, cols, dtype, like.device, stream)
+    _require_dense(out, dtype, (rows, cols), name, dev)
     return out
 
 
-def _workspace(ws, need, dev, stream):
+def _workspace(ws, need, like, dev, stream):
+    """(tensor, address, bytes) of the caller's workspace or of a new one."""
     if ws is None:
-        return _new(max(need, 16), torch.uint8, dev, stream)
+        n = max(need, 16)
+        ws = _new(1, n, torch.uint8, like.device, stream)
+        return ws, ws.data_ptr(), n
     if not isinstance(ws, torch.Tensor):
         raise TypeError("ws must be a torch.Tensor")
     _require_dense(ws, ws.dtype, ws.shape, "ws", dev)
-    return ws
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def _float_dtype(t, name):
@@ -478,12 +487,12 @@ def fp8_block_quantize(x: torch.Tensor, block_rows: int = 1, out: Optional[torch
     """x [rows, cols] as E4M3 with one power-of-two scale for each block of block_rows x 128
     values (block_rows 1: activations, 128: weights); cols % 8 == 0.  Returns (q, scales),
     q float8_e4m3fn [rows, cols], scales fp32 [ceil(rows / block_rows), ceil(cols / 128)]."""
-    dt = _float_dtype(x, "x")
-    rows, cols, dev = _require_matrix(x, x.dtype, "x")
+    dt, dev = _float_dtype(x, "x"), _here()
+    rows, cols = _require_matrix(x, x.dtype, "x", dev)
     if block_rows not in (1, BLOCK):
         raise ValueError("block_rows must be 1 or 128")
-    out = _out(out, (rows, cols), FP8, "out", dev, stream)
-    scales = _out(scales, (-(-rows // block_rows), _blocks(cols)), torch.float32, "scales", dev, stream)
+    out = _out(out, rows, cols, FP8, "out", x, dev, stream)
+    scales = _out(scales, -(-rows // block_rows), _blocks(cols), torch.float32, "scales", x, dev, stream)
     _check(_fn("fp8_block_quantize")(x.data_ptr(), dt, rows, cols, block_rows, out.data_ptr(), scales.data_ptr(),
                                      _raw_stream(stream, dev)), "fp8_block_quantize")
     return out, scales
@@ -493,34 +502,35 @@ def fp8_block_dequantize(q: torch.Tensor, scales: torch.Tensor, block_rows: int 
                          out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
                          stream=None) -> torch.Tensor:
     """The values that (q, scales) of fp8_block_quantize stand for, in out_dtype."""
-    rows, cols, dev = _require_matrix(q, FP8, "q")
+    dev = _here()
+    rows, cols = _require_matrix(q, FP8, "q", dev)
     if block_rows not in (1, BLOCK):
         raise ValueError("block_rows must be 1 or 128")
     if out_dtype not in TQ_DTYPE:
         raise TypeError("out_dtype must be fp16, bf16 or fp32")
     _require_dense(scales, torch.float32, (-(-rows // block_rows), _blocks(cols)), "scales", dev)
-    out = _out(out, (rows, cols), out_dtype, "out", dev, stream)
+    out = _out(out, rows, cols, out_dtype, "out", q, dev, stream)
     _check(_fn("fp8_block_dequantize")(q.data_ptr(), scales.data_ptr(), rows, cols, block_rows, out.data_ptr(),
                                        TQ_DTYPE[out_dtype], _raw_stream(stream, dev)), "fp8_block_dequantize")
     return out
 
 
 def _fp8_weight(w, s_w, K, dev):
-    N, wk, _ = _require_matrix(w, FP8, "w")
+    N, wk = _require_matrix(w, FP8, "w", dev)
     if wk != K:
         raise ValueError("w has %d inputs, x has %d" % (wk, K))
     _require_dense(s_w, torch.float32, (_blocks(N), _blocks(K)), "s_w", dev)
     return N
 
 
-def _fp8_out(out, out_dtype, shape, dev, accumulate, stream):
+def _fp8_out(out, out_dtype, M, N, like, dev, accumulate, stream):
     if accumulate and out is None:
         raise ValueError("accumulate needs out")
     if out_dtype is None:
         out_dtype = out.dtype if isinstance(out, torch.Tensor) else torch.bfloat16
     if out_dtype not in TQ_DTYPE:
         raise TypeError("out_dtype must be fp16, bf16 or fp32")
-    return _out(out, shape, out_dtype, "out", dev, stream)
+    return _out(out, M, N, out_dtype, "out", like, dev, stream), TQ_DTYPE[out_dtype]
 
 
 def fp8_block_gemm(x: torch.Tensor, s_x: torch.Tensor, w: torch.Tensor, s_w: torch.Tensor,
@@ -529,17 +539,18 @@ def fp8_block_gemm(x: torch.Tensor, s_x: torch.Tensor, w: torch.Tensor, s_w: tor
     """x [M, K] w [N, K]^T of E4M3 matrices with scales s_x [M, ceil(K/128)] and s_w
     [ceil(N/128), ceil(K/128)]; K % 16 == 0.  out [M, N] in out_dtype (bf16 unless out or
     out_dtype says otherwise); accumulate (fp32 out only) adds the product to out."""
-    M, K, dev = _require_matrix(x, FP8, "x")
+    dev = _here()
+    M, K = _require_matrix(x, FP8, "x", dev)
     _require_dense(s_x, torch.float32, (M, _blocks(K)), "s_x", dev)
     N = _fp8_weight(w, s_w, K, dev)
-    out = _fp8_out(out, out_dtype, (M, N), dev, accumulate, stream)
+    out, y_dt = _fp8_out(out, out_dtype, M, N, x, dev, accumulate, stream)
     _check(_fn("fp8_block_gemm")(x.data_ptr(), s_x.data_ptr(), w.data_ptr(), s_w.data_ptr(), M, N, K, out.data_ptr(),
-                                 TQ_DTYPE[out.dtype], int(accumulate), _raw_stream(stream, dev)), "fp8_block_gemm")
+                                 y_dt, accumulate, _raw_stream(stream, dev)), "fp8_block_gemm")
     return out
 
 
 def fp8_block_linear_workspace_size(M: int, N: int, K: int) -> int:
-    return int(_fn("fp8_block_linear_workspace_size")(M, N, K))
+    return _fn("fp8_block_linear_workspace_size")(M, N, K)
 
 
 def fp8_block_linear(x: torch.Tensor, w: torch.Tensor, s_w: torch.Tensor, out: Optional[torch.Tensor] = None,
@@ -547,57 +558,61 @@ def fp8_block_linear(x: torch.Tensor, w: torch.Tensor, s_w: torch.Tensor, out: O
                      ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """fp8_block_gemm of activations x [M, K] (fp16, bf16 or fp32), which are stored in
     1 x 128 E4M3 blocks on the way (as fp8_block_quantize does)."""
-    dt = _float_dtype(x, "x")
-    M, K, dev = _require_matrix(x, x.dtype, "x")
+    dt, dev = _float_dtype(x, "x"), _here()
+    M, K = _require_matrix(x, x.dtype, "x", dev)
     N = _fp8_weight(w, s_w, K, dev)
-    out = _fp8_out(out, out_dtype, (M, N), dev, accumulate, stream)
+    out, y_dt = _fp8_out(out, out_dtype, M, N, x, dev, accumulate, stream)
     need = fp8_block_linear_workspace_size(M, N, K)
     ptr, size = 0, 0
     if ws is not None or need:
-        ws = _workspace(ws, need, dev, stream)
-        ptr, size = ws.data_ptr(), ws.numel() * ws.element_size()
-    _check(_fn("fp8_block_linear")(x.data_ptr(), dt, w.data_ptr(), s_w.data_ptr(), M, N, K, out.data_ptr(),
-                                   TQ_DTYPE[out.dtype], int(accumulate), ptr, size, _raw_stream(stream, dev)),
-           "fp8_block_linear")
+        ws, ptr, size = _workspace(ws, need, x, dev, stream)
+    _check(_fn("fp8_block_linear")(x.data_ptr(), dt, w.data_ptr(), s_w.data_ptr(), M, N, K, out.data_ptr(), y_dt,
+                                   accumulate, ptr, size, _raw_stream(stream, dev)), "fp8_block_linear")
     return out
 
 
-@dataclass
 class SwigluSaved:
     """A SwiGLU block's activations in 8 bits (E4M3 and fp32 scales of 1 x 128 blocks): its
-    input x [T, D] and the projections before the activation g and u [T, F]."""
-    x: torch.Tensor
-    s_x: torch.Tensor
-    g: torch.Tensor
-    s_g: torch.Tensor
-    u: torch.Tensor
-    s_u: torch.Tensor
+    input x [T, D] with s_x [T, ceil(D/128)], and the projections before the activation g and u
+    [T, F] with s_g and s_u [T, ceil(F/128)].  One allocation, of which they are views."""
+
+    def __init__(self, T: int, D: int, F: int, device="cuda"):
+        self.T, self.D, self.F = T, D, F
+        d, f = _blocks(D), _blocks(F)
+        sizes = (T * D, 4 * T * d, T * F, 4 * T * f, T * F, 4 * T * f)
+        self._at, n = [], 0
+        for size in sizes:
+            self._at.append(n)
+            n += size + 255 & ~255
+        self.buffer = torch.empty(max(n, 256), dtype=torch.uint8, device=device)
 
     @staticmethod
     def empty(T: int, D: int, F: int, device="cuda") -> "SwigluSaved":
-        device = torch.device(device)
-        d, f = _blocks(D), _blocks(F)
-        new = torch.empty
-        return SwigluSaved(new((T, D), dtype=FP8, device=device), new((T, d), dtype=torch.float32, device=device),
-                           new((T, F), dtype=FP8, device=device), new((T, f), dtype=torch.float32, device=device),
-                           new((T, F), dtype=FP8, device=device), new((T, f), dtype=torch.float32, device=device))
+        return SwigluSaved(T, D, F, device)
+
+    def _part(self, i, cols, dtype):
+        size = self.T * cols * dtype.itemsize
+        return self.buffer[self._at[i]:self._at[i] + size].view(dtype).view(self.T, cols)
+
+    x = property(lambda self: self._part(0, self.D, FP8))
+    s_x = property(lambda self: self._part(1, _blocks(self.D), torch.float32))
+    g = property(lambda self: self._part(2, self.F, FP8))
+    s_g = property(lambda self: self._part(3, _blocks(self.F), torch.float32))
+    u = property(lambda self: self._part(4, self.F, FP8))
+    s_u = property(lambda self: self._part(5, _blocks(self.F), torch.float32))
 
     def struct(self, T: int, D: int, F: int, dev: int) -> TqSwigluSaved:
-        d, f = (T, _blocks(D)), (T, _blocks(F))
-        _require_dense(self.x, FP8, (T, D), "saved.x", dev)
-        _require_dense(self.s_x, torch.float32, d, "saved.s_x", dev)
-        _require_dense(self.g, FP8, (T, F), "saved.g", dev)
-        _require_dense(self.s_g, torch.float32, f, "saved.s_g", dev)
-        _require_dense(self.u, FP8, (T, F), "saved.u", dev)
-        _require_dense(self.s_u, torch.float32, f, "saved.s_u", dev)
-        return TqSwigluSaved(self.x.data_ptr(), self.s_x.data_ptr(), self.g.data_ptr(), self.s_g.data_ptr(),
-                             self.u.data_ptr(), self.s_u.data_ptr())
+        if (self.T, self.D, self.F) != (T, D, F):
+            raise ValueError("saved must have the shape T, D, F = %s, got %s" % ((T, D, F), (self.T, self.D, self.F)))
+        _require_dense(self.buffer, torch.uint8, self.buffer.shape, "saved", dev)
+        p = self.buffer.data_ptr()
+        return TqSwigluSaved(*[p + at for at in self._at])
 
 
-def _swiglu_weights(w_gate, w_up, dtype):
-    F, D, dev = _require_matrix(w_gate, dtype, "w_gate")
-    _require_dense(w_up, dtype, w_gate.shape, "w_up", dev)
-    return F, D, dev
+def _swiglu_weights(w_gate, w_up, dtype, dev):
+    shape = _require_matrix(w_gate, dtype, "w_gate", dev)
+    _require_dense(w_up, dtype, shape, "w_up", dev)
+    return shape
 
 
 def swiglu_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, out: Optional[torch.Tensor] = None,
@@ -605,20 +620,20 @@ def swiglu_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, ou
     """h = silu(x w_gate^T) * (x w_up^T): x [T, D], w_gate and w_up [F, D], all bf16 or all
     fp16, D and F multiples of 8; h [T, F].  `saved` receives x and the two projections in
     8 bits for swiglu_backward."""
-    dt = _float_dtype(x, "x")
-    T, D, dev = _require_matrix(x, x.dtype, "x")
-    F, wd, _ = _swiglu_weights(w_gate, w_up, x.dtype)
+    dt, dev = _float_dtype(x, "x"), _here()
+    T, D = _require_matrix(x, x.dtype, "x", dev)
+    F, wd = _swiglu_weights(w_gate, w_up, x.dtype, dev)
     if wd != D:
         raise ValueError("w_gate has %d inputs, x has %d" % (wd, D))
-    st = None if saved is None else saved.struct(T, D, F, dev)
-    out = _out(out, (T, F), x.dtype, "out", dev, stream)
-    _check(_fn("swiglu_forward")(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), dt, T, D, F, out.data_ptr(),
-                                 None if st is None else ctypes.byref(st), _raw_stream(stream, dev)), "swiglu_forward")
+    st = None if saved is None else ctypes.byref(saved.struct(T, D, F, dev))
+    out = _out(out, T, F, x.dtype, "out", x, dev, stream)
+    _check(_fn("swiglu_forward")(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), dt, T, D, F, out.data_ptr(), st,
+                                 _raw_stream(stream, dev)), "swiglu_forward")
     return out
 
 
 def swiglu_backward_workspace_size(T: int, D: int, F: int, from_saved: bool) -> int:
-    return int(_fn("swiglu_backward_workspace_size")(T, D, F, int(from_saved)))
+    return _fn("swiglu_backward_workspace_size")(T, D, F, from_saved)
 
 
 def swiglu_backward(dh: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, x: Optional[torch.Tensor] = None,
@@ -629,22 +644,21 @@ def swiglu_backward(dh: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, 
     bf16, from exactly one of x (the projections are computed again) and saved."""
     if (x is None) == (saved is None):
         raise ValueError("swiglu_backward takes exactly one of x and saved")
-    dt = _float_dtype(dh, "dh")
-    T, hf, _ = _require_matrix(dh, dh.dtype, "dh")
-    F, D, dev = _swiglu_weights(w_gate, w_up, dh.dtype)
+    dt, dev, dtype = _float_dtype(dh, "dh"), _here(), dh.dtype
+    T, hf = _require_matrix(dh, dtype, "dh", dev)
+    F, D = _swiglu_weights(w_gate, w_up, dtype, dev)
     if hf != F:
         raise ValueError("dh has %d columns, w_gate has %d outputs" % (hf, F))
     if x is not None:
-        _require_dense(x, dh.dtype, (T, D), "x", dev)
-    st = None if saved is None else saved.struct(T, D, F, dev)
-    dx = _out(dx, (T, D), dh.dtype, "dx", dev, stream)
-    dw_gate = _out(dw_gate, (F, D), dh.dtype, "dw_gate", dev, stream)
-    dw_up = _out(dw_up, (F, D), dh.dtype, "dw_up", dev, stream)
-    ws = _workspace(ws, swiglu_backward_workspace_size(T, D, F, saved is not None), dev, stream)
-    _check(_fn("swiglu_backward")(dh.data_ptr(), None if x is None else x.data_ptr(),
-                                  None if st is None else ctypes.byref(st), w_gate.data_ptr(), w_up.data_ptr(), dt, T,
-                                  D, F, dx.data_ptr(), dw_gate.data_ptr(), dw_up.data_ptr(), ws.data_ptr(),
-                                  ws.numel() * ws.element_size(), _raw_stream(stream, dev)), "swiglu_backward")
+        _require_dense(x, dtype, (T, D), "x", dev)
+    st = None if saved is None else ctypes.byref(saved.struct(T, D, F, dev))
+    dx = _out(dx, T, D, dtype, "dx", dh, dev, stream)
+    dw_gate = _out(dw_gate, F, D, dtype, "dw_gate", dh, dev, stream)
+    dw_up = _out(dw_up, F, D, dtype, "dw_up", dh, dev, stream)
+    ws, ptr, size = _workspace(ws, swiglu_backward_workspace_size(T, D, F, saved is not None), dh, dev, stream)
+    _check(_fn("swiglu_backward")(dh.data_ptr(), None if x is None else x.data_ptr(), st, w_gate.data_ptr(),
+                                  w_up.data_ptr(), dt, T, D, F, dx.data_ptr(), dw_gate.data_ptr(), dw_up.data_ptr(),
+                                  ptr, size, _raw_stream(stream, dev)), "swiglu_backward")
     return dx, dw_gate, dw_up
 
 

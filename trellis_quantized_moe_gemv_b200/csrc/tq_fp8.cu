@@ -103,15 +103,14 @@ __global__ void __launch_bounds__(256) fp8_quantize_blocks_kernel(const T *__res
     }
 }
 
-// Stored values times their scales, laid out over warps as the row kernel above.  Memory-bound.
-__global__ void __launch_bounds__(kStoreWarps * 32) fp8_dequantize_kernel(const uint8_t *__restrict__ q,
-                                                                         const float *__restrict__ scales,
-                                                                         long long rows, int cols, int block_rows,
-                                                                         void *__restrict__ out, int type) {
-    chain_entry();
+// Stored values times their scales, laid out over warps as the row kernel above: block
+// (bx, by) of store_grid.  Memory-bound.
+__device__ __forceinline__ void fp8_dequantize_block(long long bx, int by, const uint8_t *__restrict__ q,
+                                                     const float *__restrict__ scales, long long rows, int cols,
+                                                     int block_rows, void *__restrict__ out, int type) {
     const int nb = (cols + 127) / 128;
-    const long long r0 = ((long long)blockIdx.x * kStoreWarps + (threadIdx.x >> 5)) * kStoreRows;
-    const int c0 = blockIdx.y * 512 + (threadIdx.x & 31) * 8;
+    const long long r0 = (bx * kStoreWarps + (threadIdx.x >> 5)) * kStoreRows;
+    const int c0 = by * 512 + (threadIdx.x & 31) * 8;
     uint2 w[kStoreRows][2];
     float s[kStoreRows][2];
 #pragma unroll
@@ -147,6 +146,14 @@ __global__ void __launch_bounds__(kStoreWarps * 32) fp8_dequantize_kernel(const 
                                pack16(v[6], v[7], f16));
             }
         }
+}
+
+__global__ void __launch_bounds__(kStoreWarps * 32) fp8_dequantize_kernel(const uint8_t *__restrict__ q,
+                                                                         const float *__restrict__ scales,
+                                                                         long long rows, int cols, int block_rows,
+                                                                         void *__restrict__ out, int type) {
+    chain_entry();
+    fp8_dequantize_block(blockIdx.x, blockIdx.y, q, scales, rows, cols, block_rows, out, type);
 }
 
 // ------------------------------------------------------------------------------ product

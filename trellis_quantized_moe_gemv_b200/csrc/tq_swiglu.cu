@@ -382,41 +382,69 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
 }
 
-// dg and du from the 8-bit g and u: 8 values a thread, one read of g8, u8 and dh and one
-// write of dg and du.  Memory-bound.
-__global__ void __launch_bounds__(256) swiglu_grads_saved_kernel(const uint8_t *__restrict__ g8,
-                                                                 const float *__restrict__ sg,
-                                                                 const uint8_t *__restrict__ u8,
-                                                                 const float *__restrict__ su,
-                                                                 const __nv_bfloat16 *__restrict__ dh, int T, int F,
-                                                                 __nv_bfloat16 *__restrict__ dg,
-                                                                 __nv_bfloat16 *__restrict__ du) {
+// What the gradients' products read, from the 8-bit activations, in one launch: the first
+// blocks write x as bf16 (exact for scales that fp8_block_quantize made, down to bf16's least
+// subnormal), the others dg and du.  Both take two rows of 512 columns a warp, as the 8-bit
+// row kernels do.  Memory-bound.
+struct SavedArgs {
+    const uint8_t *x8, *g8, *u8;
+    const float *sx, *sg, *su;
+    const __nv_bfloat16 *dh;
+    __nv_bfloat16 *x, *dg, *du;
+    int T, D, F;
+    long long row_blocks, x_blocks;
+};
+
+__global__ void __launch_bounds__(kStoreWarps * 32) swiglu_saved_kernel(const SavedArgs p) {
     chain_entry();
-    const int per_row = F / 8, fb = (F + 127) / 128;
-    const long long n = (long long)T * per_row;
-    for (long long i = blockIdx.x * 256LL + threadIdx.x; i < n; i += gridDim.x * 256LL) {
-        const long long t = i / per_row;
-        const int f = (int)(i - t * per_row) * 8;
-        const size_t at = (size_t)t * F + f, sat = (size_t)t * fb + f / 128;
-        const uint2 gq = *reinterpret_cast<const uint2 *>(g8 + at), uq = *reinterpret_cast<const uint2 *>(u8 + at);
-        const uint4 d4 = *reinterpret_cast<const uint4 *>(dh + at);
-        const float gs = sg[sat], us = su[sat];
-        float g[8], u[8], a[8], b[8];
-        e4m3x4_to_f32(gq.x, *reinterpret_cast<float(*)[4]>(g));
-        e4m3x4_to_f32(gq.y, *reinterpret_cast<float(*)[4]>(g + 4));
-        e4m3x4_to_f32(uq.x, *reinterpret_cast<float(*)[4]>(u));
-        e4m3x4_to_f32(uq.y, *reinterpret_cast<float(*)[4]>(u + 4));
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t w2 = reinterpret_cast<const uint32_t *>(&d4)[j >> 1];
-            const float d = __uint_as_float((j & 1) ? (w2 & 0xFFFF0000u) : (w2 << 16));
-            swiglu_grads(g[j] * gs, u[j] * us, d, a[j], b[j]);
-        }
-        *reinterpret_cast<uint4 *>(dg + at) =
-            make_uint4(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(a[4], a[5]), pack_bf16(a[6], a[7]));
-        *reinterpret_cast<uint4 *>(du + at) =
-            make_uint4(pack_bf16(b[0], b[1]), pack_bf16(b[2], b[3]), pack_bf16(b[4], b[5]), pack_bf16(b[6], b[7]));
+    if (blockIdx.x < p.x_blocks) {
+        fp8_dequantize_block(blockIdx.x % p.row_blocks, (int)(blockIdx.x / p.row_blocks), p.x8, p.sx, p.T, p.D, 1, p.x,
+                             TQ_DTYPE_BF16);
+        return;
     }
+    const long long b = blockIdx.x - p.x_blocks;
+    const int F = p.F, fb = (F + 127) / 128;
+    const int r0 = (int)((b % p.row_blocks) * kStoreWarps + (threadIdx.x >> 5)) * kStoreRows;
+    const int c0 = (int)(b / p.row_blocks) * 512 + (threadIdx.x & 31) * 8;
+    uint2 gq[kStoreRows][2], uq[kStoreRows][2];
+    uint4 d4[kStoreRows][2];
+    float gs[kStoreRows][2], us[kStoreRows][2];
+#pragma unroll
+    for (int k = 0; k < kStoreRows; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int f = c0 + 256 * h;
+            if (r0 + k >= p.T || f >= F) continue;
+            const size_t at = (size_t)(r0 + k) * F + f, sat = (size_t)(r0 + k) * fb + f / 128;
+            gq[k][h] = *reinterpret_cast<const uint2 *>(p.g8 + at);
+            uq[k][h] = *reinterpret_cast<const uint2 *>(p.u8 + at);
+            d4[k][h] = *reinterpret_cast<const uint4 *>(p.dh + at);
+            gs[k][h] = p.sg[sat];
+            us[k][h] = p.su[sat];
+        }
+#pragma unroll
+    for (int k = 0; k < kStoreRows; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int f = c0 + 256 * h;
+            if (r0 + k >= p.T || f >= F) continue;
+            const size_t at = (size_t)(r0 + k) * F + f;
+            float g[8], u[8], a[8], c[8];
+            e4m3x4_to_f32(gq[k][h].x, *reinterpret_cast<float(*)[4]>(g));
+            e4m3x4_to_f32(gq[k][h].y, *reinterpret_cast<float(*)[4]>(g + 4));
+            e4m3x4_to_f32(uq[k][h].x, *reinterpret_cast<float(*)[4]>(u));
+            e4m3x4_to_f32(uq[k][h].y, *reinterpret_cast<float(*)[4]>(u + 4));
+            const uint32_t w[4] = {d4[k][h].x, d4[k][h].y, d4[k][h].z, d4[k][h].w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float d = __uint_as_float((j & 1) ? (w[j >> 1] & 0xFFFF0000u) : (w[j >> 1] << 16));
+                swiglu_grads(g[j] * gs[k][h], u[j] * us[k][h], d, a[j], c[j]);
+            }
+            *reinterpret_cast<uint4 *>(p.dg + at) =
+                make_uint4(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(a[4], a[5]), pack_bf16(a[6], a[7]));
+            *reinterpret_cast<uint4 *>(p.du + at) =
+                make_uint4(pack_bf16(c[0], c[1]), pack_bf16(c[2], c[3]), pack_bf16(c[4], c[5]), pack_bf16(c[6], c[7]));
+        }
 }
 
 // ------------------------------------------------------------------------------ host side
@@ -628,17 +656,29 @@ TQ_API int swiglu_backward(const void *dh, const void *x, const tq_swiglu_saved 
     if (st) return st;
     const void *xb = x;
     if (saved) {
-        // x as bf16: exact, an E4M3 value times a power of two (down to bf16's least subnormal)
-        st = fp8_block_dequantize(saved->x, saved->s_x, T, D, 1, w, TQ_DTYPE_BF16, stream);
-        if (st) return st;
+        SavedArgs a{};
+        a.x8 = saved->x;
+        a.g8 = saved->g;
+        a.u8 = saved->u;
+        a.sx = saved->s_x;
+        a.sg = saved->s_g;
+        a.su = saved->s_u;
+        a.dh = p.dh;
+        a.x = reinterpret_cast<__nv_bfloat16 *>(w);
+        a.dg = p.dg;
+        a.du = p.du;
+        a.T = T;
+        a.D = D;
+        a.F = F;
+        const dim3 gx = store_grid(T, D), gf = store_grid(T, F);
+        a.row_blocks = gx.x;
+        a.x_blocks = (long long)gx.x * gx.y;
+        const long long blocks = a.x_blocks + (long long)gf.x * gf.y;
+        if (blocks > 0x7FFFFFFFLL) return TQ_ERR_UNSUPPORTED;
         xb = w;
-        const long long n = (long long)T * (F / 8);
-        const long long blocks = (n + 255) / 256, most = 8LL * num_sms();
         LaunchScope ls(s, kStageSwigluGrad);
-        if (launch_chained(swiglu_grads_saved_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, s,
-                           (const uint8_t *)saved->g, (const float *)saved->s_g, (const uint8_t *)saved->u,
-                           (const float *)saved->s_u, p.dh, T, F, p.dg, p.du) != cudaSuccess)
-            return record_cuda_error("swiglu_grads_saved_kernel");
+        if (launch_chained(swiglu_saved_kernel, dim3((unsigned)blocks), dim3(kStoreWarps * 32), 0, s, a) != cudaSuccess)
+            return record_cuda_error("swiglu_saved_kernel");
     } else {
         st = pair_map(&maps.a0, x, T, D, 0);
         if (st) return st;
