@@ -409,9 +409,9 @@ def _blocks(n: int) -> int:
     return -(-n // BLOCK)
 
 
-def _here() -> int:
-    """The current device, where the kernels run (before CUDA is in use there is none)."""
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else -1
+def _here(t) -> int:
+    """The current device, where the kernels run; -1 where t is not on a GPU (it is then refused)."""
+    return torch._C._cuda_getDevice() if isinstance(t, torch.Tensor) and t.is_cuda else -1
 
 
 # The checks below decide the usual case in one expression and look for the reason only where it
@@ -477,9 +477,10 @@ def _workspace(ws, need, like, dev, stream):
 
 
 def _float_dtype(t, name):
-    if not isinstance(t, torch.Tensor) or t.dtype not in TQ_DTYPE:
+    dt = TQ_DTYPE.get(getattr(t, "dtype", None))
+    if dt is None:
         raise TypeError("%s must be an fp16, bf16 or fp32 tensor" % name)
-    return TQ_DTYPE[t.dtype]
+    return dt
 
 
 def fp8_block_quantize(x: torch.Tensor, block_rows: int = 1, out: Optional[torch.Tensor] = None,
@@ -487,7 +488,7 @@ def fp8_block_quantize(x: torch.Tensor, block_rows: int = 1, out: Optional[torch
     """x [rows, cols] as E4M3 with one power-of-two scale for each block of block_rows x 128
     values (block_rows 1: activations, 128: weights); cols % 8 == 0.  Returns (q, scales),
     q float8_e4m3fn [rows, cols], scales fp32 [ceil(rows / block_rows), ceil(cols / 128)]."""
-    dt, dev = _float_dtype(x, "x"), _here()
+    dt, dev = _float_dtype(x, "x"), _here(x)
     rows, cols = _require_matrix(x, x.dtype, "x", dev)
     if block_rows not in (1, BLOCK):
         raise ValueError("block_rows must be 1 or 128")
@@ -502,7 +503,7 @@ def fp8_block_dequantize(q: torch.Tensor, scales: torch.Tensor, block_rows: int 
                          out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
                          stream=None) -> torch.Tensor:
     """The values that (q, scales) of fp8_block_quantize stand for, in out_dtype."""
-    dev = _here()
+    dev = _here(q)
     rows, cols = _require_matrix(q, FP8, "q", dev)
     if block_rows not in (1, BLOCK):
         raise ValueError("block_rows must be 1 or 128")
@@ -539,7 +540,7 @@ def fp8_block_gemm(x: torch.Tensor, s_x: torch.Tensor, w: torch.Tensor, s_w: tor
     """x [M, K] w [N, K]^T of E4M3 matrices with scales s_x [M, ceil(K/128)] and s_w
     [ceil(N/128), ceil(K/128)]; K % 16 == 0.  out [M, N] in out_dtype (bf16 unless out or
     out_dtype says otherwise); accumulate (fp32 out only) adds the product to out."""
-    dev = _here()
+    dev = _here(x)
     M, K = _require_matrix(x, FP8, "x", dev)
     _require_dense(s_x, torch.float32, (M, _blocks(K)), "s_x", dev)
     N = _fp8_weight(w, s_w, K, dev)
@@ -558,7 +559,7 @@ def fp8_block_linear(x: torch.Tensor, w: torch.Tensor, s_w: torch.Tensor, out: O
                      ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """fp8_block_gemm of activations x [M, K] (fp16, bf16 or fp32), which are stored in
     1 x 128 E4M3 blocks on the way (as fp8_block_quantize does)."""
-    dt, dev = _float_dtype(x, "x"), _here()
+    dt, dev = _float_dtype(x, "x"), _here(x)
     M, K = _require_matrix(x, x.dtype, "x", dev)
     N = _fp8_weight(w, s_w, K, dev)
     out, y_dt = _fp8_out(out, out_dtype, M, N, x, dev, accumulate, stream)
@@ -620,7 +621,7 @@ def swiglu_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, ou
     """h = silu(x w_gate^T) * (x w_up^T): x [T, D], w_gate and w_up [F, D], all bf16 or all
     fp16, D and F multiples of 8; h [T, F].  `saved` receives x and the two projections in
     8 bits for swiglu_backward."""
-    dt, dev = _float_dtype(x, "x"), _here()
+    dt, dev = _float_dtype(x, "x"), _here(x)
     T, D = _require_matrix(x, x.dtype, "x", dev)
     F, wd = _swiglu_weights(w_gate, w_up, x.dtype, dev)
     if wd != D:
@@ -644,7 +645,7 @@ def swiglu_backward(dh: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, 
     bf16, from exactly one of x (the projections are computed again) and saved."""
     if (x is None) == (saved is None):
         raise ValueError("swiglu_backward takes exactly one of x and saved")
-    dt, dev, dtype = _float_dtype(dh, "dh"), _here(), dh.dtype
+    dt, dev, dtype = _float_dtype(dh, "dh"), _here(dh), dh.dtype
     T, hf = _require_matrix(dh, dtype, "dh", dev)
     F, D = _swiglu_weights(w_gate, w_up, dtype, dev)
     if hf != F:
