@@ -334,7 +334,8 @@ int fp8_block_dequantize(const uint8_t *q, const float *scales, int64_t rows, in
  *   x : [M][K] E4M3, s_x : [M][ceil(K / 128)] fp32.
  *   w : [N][K] E4M3, s_w : [ceil(N / 128)][ceil(K / 128)] fp32.
  *   y : [M][N] of y_dtype (F16, BF16 or F32); accumulate != 0 (F32 only): y += the product.
- *   K % 16 == 0; M and N any size; all arrays 16-byte aligned.
+ *   K % 16 == 0; M and N any size (up to 2^31 - 1024); all arrays 16-byte aligned; y overlaps
+ *   no input.
  * fp8_block_linear -- the same from activations x [M][K] of x_dtype (F16, BF16 or F32),
  * which are quantised as fp8_block_quantize (block_rows 1) does on the way.  ws: device
  * workspace of fp8_block_linear_workspace_size(M, N, K) bytes, 16-byte aligned; 0 bytes (ws
@@ -366,7 +367,7 @@ typedef struct {
  * swiglu_forward -- h = silu(g) * u with g = x W_gate^T, u = x W_up^T, in one kernel (fp32
  * sums; g and u are not rounded, h once).
  *   x : [T][D], w_gate, w_up : [F][D], h : [T][F], all of dtype (F16 or BF16), 16-byte
- *   aligned.  D % 8 == 0, F % 8 == 0.
+ *   aligned.  D % 8 == 0, F % 8 == 0 (each size up to 2^31 - 1024).  Outputs overlap no input.
  *   saved: NULL, or the arrays that receive x, g and u in 8 bits (g and u are stored from
  *   their fp32 sums by the same kernel); h is the same either way up to the order of its sums.
  */

@@ -57,6 +57,7 @@ def test_products(lib):
     assert g(FAKE, FAKE, FAKE, FAKE, 4, 4, 128, FAKE, 9, 0, None) == INVALID
     assert g(FAKE, FAKE, FAKE, FAKE, 4, 4, 128, FAKE, BF16, 1, None) == UNSUPPORTED  # accumulate in 16 bits
     assert g(FAKE, None, FAKE, FAKE, 4, 4, 128, FAKE, F32, 0, None) == INVALID
+    assert g(FAKE, FAKE, FAKE, FAKE, (1 << 31) - 1, 4, 128, FAKE, F32, 0, None) == UNSUPPORTED
     assert g(FAKE, FAKE, MISALIGNED, FAKE, 4, 4, 128, FAKE, F32, 0, None) == ALIGNMENT
     assert g(None, None, None, None, 0, 4, 128, None, F32, 0, None) == OK
     assert g(None, None, None, None, 4, 0, 128, None, F32, 0, None) == OK
@@ -91,6 +92,7 @@ def test_swiglu(lib, api):
     assert f(FAKE, FAKE, FAKE, BF16, 4, 128, 60, FAKE, None, None) == INVALID        # F % 8
     assert f(FAKE, FAKE, FAKE, BF16, -4, 128, 64, FAKE, None, None) == INVALID
     assert f(FAKE, None, FAKE, BF16, 4, 128, 64, FAKE, None, None) == INVALID
+    assert f(FAKE, FAKE, FAKE, BF16, (1 << 31) - 8, 128, 64, FAKE, None, None) == UNSUPPORTED
     assert f(FAKE, FAKE, MISALIGNED, BF16, 4, 128, 64, FAKE, None, None) == ALIGNMENT
     assert f(FAKE, FAKE, FAKE, BF16, 4, 128, 64, FAKE, _saved(api, s_g=None), None) == INVALID
     assert f(FAKE, FAKE, FAKE, BF16, 4, 128, 64, FAKE, _saved(api, u=0x10004), None) == ALIGNMENT

@@ -110,7 +110,11 @@ def test_quantize_writes_nothing_else(api):
 # ----------------------------------------------------------------------------- FP8 product
 
 SHAPES = [(1, 1, 16), (1, 128, 128), (2, 7, 112), (16, 129, 144), (17, 256, 384), (33, 1001, 272), (64, 200, 2064),
-          (65, 64, 128), (128, 300, 1040), (129, 130, 128), (255, 256, 256), (257, 1000, 400), (520, 513, 1168)]
+          (65, 64, 128), (128, 300, 1040), (129, 130, 128), (255, 256, 256), (257, 1000, 400), (520, 513, 1168),
+          # the pair kernel: several rounds of tiles, a ragged one in every size
+          (1300, 1500, 272), (257, 9503, 144), (2100, 1030, 1168), (4100, 5000, 48),
+          # one launch up to 128 blocks of a row, two beyond
+          (9, 513, 2048), (16, 200, 1024), (16, 200, 8208), (3, 20000, 2064)]
 
 
 def exact_operands(M, N, K, seed):
@@ -156,7 +160,7 @@ def test_linear(api, dtype, M, N, K):
     assert y16.dtype == BF16 and torch.equal(y16, got.to(BF16))
 
 
-@pytest.mark.parametrize("M", [5, 200])
+@pytest.mark.parametrize("M", [5, 200, 6500])
 def test_product_keeps_nan_to_its_row_and_writes_nothing_else(api, M):
     N, K = 301, 272
     x, s_x, w, s_w = exact_operands(M, N, K, 5)
@@ -203,7 +207,9 @@ def forward_oracle(x, a, b):
 
 
 T_SHAPES = [(1, 8, 8), (1, 128, 64), (2, 136, 72), (7, 1000, 504), (16, 256, 128), (17, 512, 200), (33, 64, 1000),
-            (64, 264, 136), (128, 1032, 264), (129, 128, 128), (256, 256, 256), (300, 1000, 504), (513, 72, 392)]
+            (64, 264, 136), (128, 1032, 264), (129, 128, 128), (256, 256, 256), (300, 1000, 504), (513, 72, 392),
+            # the pair kernel: one round, a last round halved in width, several rounds
+            (1280, 72, 1280), (2000, 136, 1400), (4100, 64, 2600)]
 
 
 @pytest.mark.parametrize("dtype", [BF16, F16])
@@ -261,7 +267,9 @@ def grads_oracle(g, u, dh, x, a, b, eg, eu):
 
 
 B_SHAPES = [(1, 8, 8), (1, 128, 64), (3, 136, 72), (64, 64, 64), (65, 264, 200), (128, 256, 256), (200, 1000, 136),
-            (257, 520, 264), (300, 72, 504)]
+            (257, 520, 264), (300, 72, 504),
+          # tiles halved in width, whole, and whole with dx tiles filling up behind uneven dw tiles
+          (700, 1032, 392), (1500, 1096, 1200), (1300, 2600, 1400)]
 
 
 @pytest.mark.parametrize("T,D,F", B_SHAPES)
@@ -291,7 +299,8 @@ def test_backward_from_saved(api, T, D, F):
         close(y, w, t, BF16)
 
 
-@pytest.mark.parametrize("T,D,F", [(1, 8, 8), (70, 200, 136), (64, 256, 256), (200, 264, 320), (130, 520, 72)])
+@pytest.mark.parametrize("T,D,F", [(1, 8, 8), (70, 200, 136), (64, 256, 256), (200, 264, 320), (130, 520, 72),
+                                   (1500, 1096, 1200), (1300, 2600, 1400)])
 def test_gradients_of_integers_are_exact(api, T, D, F):
     """g = 64 makes s = 1 in fp32 (e^-64 < 2^-24), so dg = dh u and du = 64 dh: with integers
     every product and sum is exact, and the result is the exact sum rounded once to bf16."""

@@ -296,6 +296,9 @@ __device__ __forceinline__ void grouped_tile(long long t, int m_tiles, int n_til
 
 // ------------------------------------------------------------------------------ host
 
+// Largest size the tile arithmetic takes (sizes are rounded up to tiles in 32 bits).
+constexpr int kMostSize = 0x7FFFFFFF - 1023;
+
 // Tensor map of a row-major [rows][cols] matrix (rows packed) read in boxes of
 // box_rows x one 128-byte row segment, 128-byte swizzle, zeros outside the matrix.
 static int matrix_map(CUtensorMap *map, CUtensorMapDataType type, size_t esize, const void *base, long long rows,

@@ -458,6 +458,7 @@ static int fp8_product_status(int M, int N, int K, int y_dtype, int accumulate) 
     if (M < 0 || N < 0 || K < 1 || K % 16) return TQ_ERR_INVALID_ARG;
     if (y_dtype < TQ_DTYPE_F16 || y_dtype > TQ_DTYPE_F32) return TQ_ERR_INVALID_ARG;
     if (accumulate && y_dtype != TQ_DTYPE_F32) return TQ_ERR_UNSUPPORTED;
+    if (M > kMostSize || N > kMostSize || K > kMostSize) return TQ_ERR_UNSUPPORTED;
     return TQ_OK;
 }
 
@@ -490,6 +491,7 @@ TQ_API int fp8_block_quantize(const void *x, int x_dtype, int64_t rows, int cols
     if (x_dtype < TQ_DTYPE_F16 || x_dtype > TQ_DTYPE_F32 || rows < 0 || cols < 1 || cols % 8 ||
         (block_rows != 1 && block_rows != 128))
         return TQ_ERR_INVALID_ARG;
+    if (cols > kMostSize) return TQ_ERR_UNSUPPORTED;
     if (rows == 0) return TQ_OK;
     if (block_rows == 128 ? (rows + 127) / 128 * ((cols + 127LL) / 128) > 0x7FFFFFFFLL : !store_grid_fits(rows, cols))
         return TQ_ERR_UNSUPPORTED;
@@ -509,6 +511,7 @@ TQ_API int fp8_block_dequantize(const uint8_t *q, const float *scales, int64_t r
     if (out_dtype < TQ_DTYPE_F16 || out_dtype > TQ_DTYPE_F32 || rows < 0 || cols < 1 || cols % 8 ||
         (block_rows != 1 && block_rows != 128))
         return TQ_ERR_INVALID_ARG;
+    if (cols > kMostSize) return TQ_ERR_UNSUPPORTED;
     if (rows == 0) return TQ_OK;
     if (!store_grid_fits(rows, cols)) return TQ_ERR_UNSUPPORTED;
     if (!q || !scales || !out) return TQ_ERR_INVALID_ARG;
@@ -532,7 +535,7 @@ TQ_API int fp8_block_gemm(const uint8_t *x, const float *s_x, const uint8_t *w, 
 }
 
 TQ_API size_t fp8_block_linear_workspace_size(int M, int N, int K) {
-    if (M < 0 || N < 0 || K < 1 || K % 16 || tq::fp8_fused_case(M, N, K)) return 0;
+    if (tq::fp8_product_status(M, N, K, TQ_DTYPE_F32, 0) || M == 0 || N == 0 || tq::fp8_fused_case(M, N, K)) return 0;
     const size_t q = ((size_t)M * K + 255) & ~(size_t)255;
     return q + (((size_t)M * ((K + 127) / 128) * 4 + 255) & ~(size_t)255);
 }

@@ -526,6 +526,7 @@ static inline size_t align256_d(size_t n) { return (n + 255) & ~(size_t)255; }
 
 static int swiglu_shape_status(int T, int D, int F) {
     if (T < 0 || D < 1 || F < 1 || D % 8 || F % 8) return TQ_ERR_INVALID_ARG;
+    if (T > kMostSize || D > kMostSize || F > kMostSize) return TQ_ERR_UNSUPPORTED;
     return TQ_OK;
 }
 
