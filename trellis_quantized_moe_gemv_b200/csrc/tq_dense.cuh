@@ -9,6 +9,11 @@
 
 namespace tq {
 
+// Stage tags of this file's users (tq_profile_*), after those of Stage.
+constexpr int kStageSwiglu = kNumStages, kStageSwigluGrad = kNumStages + 1, kStageFp8Store = kNumStages + 2,
+              kStageFp8Gemm = kNumStages + 3;
+static_assert(kStageSwiglu == 15, "the C header documents the numbers");
+
 // ------------------------------------------------------------------------------ cluster
 
 __device__ __forceinline__ uint32_t cluster_rank() {
