@@ -446,6 +446,44 @@ def test_a_captured_step_replays_on_new_inputs_and_two_share_a_workspace(api, T)
                 assert torch.equal(t, w)
 
 
+def test_first_calls_of_one_size_allow_capture_of_another():
+    """In a process of its own: after one eager call of each entry point, other sizes (other
+    kernels of the same entry points) are captured on their first call."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+from trellis_quantized_moe_gemv_b200 import api
+def state(T, D, F):
+    g = torch.Generator().manual_seed(T)
+    r = lambda *n: (torch.randn(*n, generator=g)).bfloat16().cuda()
+    return r(T, D), r(F, D) / 8, r(F, D) / 8, r(T, F), *api.fp8_block_quantize(r(96, D), 128)
+def calls(x, a, b, dh, w, s_w):
+    saved = api.SwigluSaved(x.shape[0], x.shape[1], a.shape[0])
+    h = api.swiglu_forward(x, a, b)
+    h2 = api.swiglu_forward(x, a, b, saved=saved)
+    return (h, h2, *api.swiglu_backward(dh, a, b, x=x), *api.swiglu_backward(dh, a, b, saved=saved),
+            api.fp8_block_linear(x, w, s_w, out_dtype=torch.float32),
+            api.fp8_block_gemm(saved.x, saved.s_x, w, s_w, out_dtype=torch.float32))
+calls(*state(1, 64, 64))
+torch.cuda.synchronize()
+for T, F in ((17, 64), (40, 64), (100, 64), (1000, 2400)):
+    s = state(T, 264 * 16, F) if F == 64 else state(T, 64, F)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = calls(*s)
+    g.replay()
+    torch.cuda.synchronize()
+    for x, y in zip(out, calls(*s)):
+        assert torch.equal(x, y)
+print("captured", api.device_status())
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "captured 0", r.stdout + r.stderr
+
+
 def test_on_another_stream(api):
     T, D, F = 100, 272, 136
     s = step_state(api, T, D, F, 70)

@@ -52,8 +52,8 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
 
 // Arrival on a barrier of another CTA that hands over tensor memory which this thread has
 // finished reading (its loads waited for): no generic memory is handed over, so it needs no
-// release, whose cluster-wide fence stalled the accumulator loop (309 -> XXX us, 8192 x 4096
-// x 4096 E4M3).
+// release, whose cluster-wide fence stalled the accumulator loop (8192 x 4096 x 4096 in E4M3:
+// 311 us with it, 195 without).
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
@@ -300,6 +300,15 @@ __device__ __forceinline__ void grouped_tile(long long t, int m_tiles, int n_til
 }
 
 // ------------------------------------------------------------------------------ host
+
+// Lets a kernel use `bytes` of dynamic shared memory on the current device, and loads it.
+template <typename... KArgs>
+static bool set_smem(void (*kernel)(KArgs...), int bytes) {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, kernel) != cudaSuccess ||
+           (bytes > 0 &&
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess);
+}
 
 // Largest size the tile arithmetic takes (sizes are rounded up to tiles in 32 bits).
 constexpr int kMostSize = 0x7FFFFFFF - 1023;

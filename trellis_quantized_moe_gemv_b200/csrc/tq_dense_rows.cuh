@@ -372,16 +372,14 @@ inline int rows_share(int width, int kblocks) {
 }
 
 template <int N, int KIND>
+static bool configure_rows() {
+    return set_smem(dense_rows_kernel<N, KIND>, RowsShape<N, KIND>::kBytes);
+}
+
+template <int N, int KIND>
 static int launch_rows(const CUtensorMap &w0, const CUtensorMap &w1, const CUtensorMap &x, const RowsArgs &a,
                        cudaStream_t s, bool chained) {
     using SH = RowsShape<N, KIND>;
-    static PerDeviceFlag configured;
-    if (!configured.get()) {
-        if (cudaFuncSetAttribute(dense_rows_kernel<N, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, SH::kBytes) !=
-            cudaSuccess)
-            return record_cuda_error("cudaFuncSetAttribute(dense_rows_kernel)");
-        configured.set();
-    }
     const int per_tile = KIND == kSwiglu ? 64 : kRowsM;
     const long long row_tiles = (a.width + (long long)per_tile - 1) / per_tile;
     const int token_tiles = (a.rows + N - 1) / N;

@@ -388,6 +388,24 @@ static bool fp8_fused_case(int M, int N, int K) {
     return share <= RowsStore<16>::kMost && M * share <= 128;
 }
 
+static bool configure_store() {
+    return set_smem(fp8_quantize_rows_kernel<__half>, 0) || set_smem(fp8_quantize_rows_kernel<__nv_bfloat16>, 0) ||
+           set_smem(fp8_quantize_rows_kernel<float>, 0);
+}
+
+// The first product on a device sets up every kernel that a later one may launch (their launch
+// attributes; loading them), so that later calls may be captured.
+static int configure_fp8() {
+    static PerDeviceFlag configured;
+    if (configured.get()) return TQ_OK;
+    if (set_smem(fp8_pair_kernel, (int)sizeof(Fp8Smem) + 1024) || configure_rows<16, kFp8>() ||
+        configure_rows<32, kFp8>() || configure_rows<64, kFp8>() || configure_rows<128, kFp8>() ||
+        configure_rows<16, kFp8Store>() || configure_store())
+        return record_cuda_error("configure_fp8");
+    configured.set();
+    return TQ_OK;
+}
+
 static int fp8_product(const uint8_t *x8, const float *sx, const uint8_t *w8, const float *sw, int M, int N, int K,
                        void *y, int y_dtype, int accumulate, cudaStream_t s) {
     RowsArgs a{};
@@ -417,13 +435,7 @@ static int fp8_product(const uint8_t *x8, const float *sx, const uint8_t *w8, co
     }
     st = matrix_map(&mx, u8, 1, x8, M, K, 128);
     if (st) return st;
-    static PerDeviceFlag configured;
     const int smem = (int)sizeof(Fp8Smem) + 1024;
-    if (!configured.get()) {
-        if (cudaFuncSetAttribute(fp8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-            return record_cuda_error("cudaFuncSetAttribute(fp8_pair_kernel)");
-        configured.set();
-    }
     const long long tiles = ((M + 255LL) / 256) * ((N + 255LL) / 256), pairs = num_sms() / 2;
     LaunchScope ls(s, kStageFp8Gemm);
     if (launch_chained(fp8_pair_kernel, dim3(2 * (unsigned)(tiles < pairs ? tiles : pairs)), dim3(kFp8Threads), smem, s,
@@ -531,6 +543,7 @@ TQ_API int fp8_block_gemm(const uint8_t *x, const float *s_x, const uint8_t *w, 
     if (st || M == 0 || N == 0) return st;
     if (!x || !s_x || !w || !s_w || !y) return TQ_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned16(w) || !aligned16(y) || !aligned16(s_x) || !aligned16(s_w)) return TQ_ERR_ALIGNMENT;
+    if (const int c = configure_fp8()) return c;
     return fp8_product(x, s_x, w, s_w, M, N, K, y, y_dtype, accumulate, (cudaStream_t)stream);
 }
 
@@ -549,9 +562,11 @@ TQ_API int fp8_block_linear(const void *x, int x_dtype, const uint8_t *w, const 
     if (!x || !w || !s_w || !y) return TQ_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned16(w) || !aligned16(y) || !aligned16(s_w) || (ws && !aligned16(ws)))
         return TQ_ERR_ALIGNMENT;
-    if (fp8_fused_case(M, N, K))
+    const bool fused = fp8_fused_case(M, N, K);
+    if (!fused && (!ws || ws_bytes < fp8_block_linear_workspace_size(M, N, K))) return TQ_ERR_WORKSPACE;
+    if ((st = configure_fp8())) return st;
+    if (fused)
         return fp8_product_fused(x, x_dtype, w, s_w, M, N, K, y, y_dtype, accumulate, (cudaStream_t)stream);
-    if (!ws || ws_bytes < fp8_block_linear_workspace_size(M, N, K)) return TQ_ERR_WORKSPACE;
     uint8_t *q = reinterpret_cast<uint8_t *>(ws);
     float *sx = reinterpret_cast<float *>(q + (((size_t)M * K + 255) & ~(size_t)255));
     st = fp8_block_quantize(x, x_dtype, M, K, 1, q, sx, stream);

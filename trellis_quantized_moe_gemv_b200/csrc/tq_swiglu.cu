@@ -17,9 +17,10 @@
 //     over the tokens) and then those of dx (A K-major, B MN-major; K runs over Wg's rows
 //     and then Wu's), so the long weight-gradient tiles start first and the dx tiles fill
 //     the pairs that finish early.
-// dg and du are rounded to bf16 between the two launches: the tensor cores take 16-bit
-// operands, and a rounding of 2^-9 in independent terms of a sum changes the sum by less
-// than the rounding of the 16-bit gradient itself.
+// dg and du are rounded to bf16 between the two launches, because the tensor cores take 16-bit
+// operands: at most 2^-8 of each term, and as the terms' errors are independent about as much
+// of a sum as the rounding of the 16-bit gradient itself (measured against 64 bits: 0.0024 of
+// the gradients' norm, 0.0017 for the last rounding alone).
 //
 // Few tokens: dense_rows_kernel (weights streamed once, tokens on the MMA's N side).
 #include "tq_dense_rows.cuh"
@@ -456,8 +457,9 @@ static int pair_map(CUtensorMap *m, const void *base, long long rows, long long 
 
 // Gate/up tiles: where the last round over the pairs would leave half of them or more without
 // work, its tiles are halved in width (not where they store 8-bit blocks, which need all
-// 128 columns).  8192 tokens, 4096 -> 1024: 256 tiles on 74 pairs are 3 rounds and 34 tiles, or 68
-// halves; %s.
+// 128 columns).  8192 tokens, 4096 -> 1024: 256 tiles on 74 pairs are 3 rounds and 34 tiles, run
+// as 68 halves.  It pays where there are few rounds (1111 tokens, 1000 -> 504, 20 tiles as 40: the
+// gradient's two launches 25.6 -> 20.6 us); over several rounds the power limit gives the time back.
 static long long plan_gateup(PairArgs &p, long long pairs, bool may_halve) {
     const long long n = (((long long)p.T + kPairM - 1) / kPairM) * ((p.F + 127LL) / 128), last = n % pairs;
     p.full = may_halve && 2 * last <= pairs ? n - last : n;
@@ -505,14 +507,7 @@ static long long plan_grads(PairArgs &p, long long pairs) {
 
 template <int KIND>
 static int launch_pair(const PairMaps &maps, PairArgs p, cudaStream_t s, int stage) {
-    static PerDeviceFlag configured;
     const int smem = (int)sizeof(PairSmem) + 1024;
-    if (!configured.get()) {
-        if (cudaFuncSetAttribute(pair_gemm_kernel<KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-            cudaSuccess)
-            return record_cuda_error("cudaFuncSetAttribute(pair_gemm_kernel)");
-        configured.set();
-    }
     const long long pairs = num_sms() / 2;
     const long long tiles = KIND == kPairGrads ? plan_grads(p, pairs) : plan_gateup(p, pairs, KIND != kPairSave);
     const unsigned grid = 2 * (unsigned)(tiles < pairs ? tiles : pairs);
@@ -520,6 +515,21 @@ static int launch_pair(const PairMaps &maps, PairArgs p, cudaStream_t s, int sta
     if (launch_chained(pair_gemm_kernel<KIND>, dim3(grid), dim3(kPairThreads), smem, s, maps, p) != cudaSuccess)
         return record_cuda_error("pair_gemm_kernel");
     return launch_status();
+}
+
+// The first call of an entry point on a device sets up every kernel that a later call of it may
+// launch (their launch attributes; loading them), so that later calls may be captured.
+static int configure_swiglu() {
+    static PerDeviceFlag configured;
+    if (configured.get()) return TQ_OK;
+    const int smem = (int)sizeof(PairSmem) + 1024;
+    if (set_smem(pair_gemm_kernel<kPairForward>, smem) || set_smem(pair_gemm_kernel<kPairSave>, smem) ||
+        set_smem(pair_gemm_kernel<kPairRecompute>, smem) || set_smem(pair_gemm_kernel<kPairGrads>, smem) ||
+        configure_rows<16, kSwiglu>() || configure_rows<32, kSwiglu>() || configure_rows<64, kSwiglu>() ||
+        configure_rows<128, kSwiglu>() || set_smem(swiglu_saved_kernel, 0) || configure_store())
+        return record_cuda_error("configure_swiglu");
+    configured.set();
+    return TQ_OK;
 }
 
 static inline size_t align256_d(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -581,6 +591,7 @@ TQ_API int swiglu_forward(const void *x, const void *w_gate, const void *w_up, i
     if (!x || !w_gate || !w_up || !h || (saved && !saved_complete(saved))) return TQ_ERR_INVALID_ARG;
     if (!aligned16(x) || !aligned16(w_gate) || !aligned16(w_up) || !aligned16(h) || (saved && !saved_aligned(saved)))
         return TQ_ERR_ALIGNMENT;
+    if ((st = configure_swiglu())) return st;
     const cudaStream_t s = (cudaStream_t)stream;
     const int f16 = dtype == TQ_DTYPE_F16;
     if (!saved && swiglu_rows_case(T, F)) return swiglu_rows(x, w_gate, w_up, f16, T, D, F, h, s);
@@ -637,6 +648,7 @@ TQ_API int swiglu_backward(const void *dh, const void *x, const tq_swiglu_saved 
         return TQ_ERR_ALIGNMENT;
     if (!ws || ws_bytes < swiglu_backward_workspace_size(T, D, F, saved != nullptr)) return TQ_ERR_WORKSPACE;
 
+    if ((st = configure_swiglu())) return st;
     char *w = reinterpret_cast<char *>(ws);
     PairArgs p{};
     p.T = T;
