@@ -384,7 +384,8 @@ int swiglu_forward(const void *x, const void *w_gate, const void *w_up, int dtyp
  * added), do not depend on the order of execution, and must not overlap the inputs.
  *   dtype: BF16 (F16: TQ_ERR_UNSUPPORTED, its range does not hold dg and du).
  *   dx : [T][D], dw_gate, dw_up : [F][D].  ws: device workspace of
- *   swiglu_backward_workspace_size(T, D, F, saved != NULL) bytes, 16-byte aligned.
+ *   swiglu_backward_workspace_size(T, D, F, saved != NULL) bytes, 16-byte aligned (the size
+ *   depends on the device's SM count: query it on the device that runs the call).
  *   T = 0 writes zero weight gradients.
  */
 size_t swiglu_backward_workspace_size(int T, int D, int F, int from_saved);

@@ -269,7 +269,9 @@ def grads_oracle(g, u, dh, x, a, b, eg, eu):
 B_SHAPES = [(1, 8, 8), (1, 128, 64), (3, 136, 72), (64, 64, 64), (65, 264, 200), (128, 256, 256), (200, 1000, 136),
             (257, 520, 264), (300, 72, 504),
           # tiles halved in width, whole, and whole with dx tiles filling up behind uneven dw tiles
-          (700, 1032, 392), (1500, 1096, 1200), (1300, 2600, 1400)]
+          (700, 1032, 392), (1500, 1096, 1200), (1300, 2600, 1400),
+          # K of the weight gradients split (many tokens), of dx (wide F), of both
+          (8000, 136, 72), (4100, 520, 264), (70, 264, 4000), (1000, 72, 2056)]
 
 
 @pytest.mark.parametrize("T,D,F", B_SHAPES)
@@ -300,7 +302,8 @@ def test_backward_from_saved(api, T, D, F):
 
 
 @pytest.mark.parametrize("T,D,F", [(1, 8, 8), (70, 200, 136), (64, 256, 256), (200, 264, 320), (130, 520, 72),
-                                   (1500, 1096, 1200), (1300, 2600, 1400)])
+                                   (1500, 1096, 1200), (1300, 2600, 1400), (8000, 136, 72), (70, 264, 4000),
+                                   (1000, 72, 2056)])
 def test_gradients_of_integers_are_exact(api, T, D, F):
     """g = 64 makes s = 1 in fp32 (e^-64 < 2^-24), so dg = dh u and du = 64 dh: with integers
     every product and sum is exact, and the result is the exact sum rounded once to bf16."""

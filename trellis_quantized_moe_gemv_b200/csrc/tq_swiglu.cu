@@ -64,18 +64,21 @@ struct PairArgs {
     long long full;                           // gate/up: whole tiles; the others are halved
     long long tiles;                          // gate/up: tiles, halves counted one by one
     int halved;                               // gradients: every tile is half as wide
-    long long n_dw, n_dx;                     // gradients: tiles of each kind
-    int more;                                 // gradients: pairs that have one dw tile more than the rest,
-    long long dx_more, dx_rest;               //   and the dx tiles of such a pair and of another
+    int split_dw, split_dx;                   // gradients: pieces that K of a tile is cut into
+    long long n_dw, n_dx;                     // gradients: pieces of each kind
+    int more;                                 // gradients: pairs that have one dw piece more than the rest,
+    long long dx_more, dx_rest;               //   and the dx pieces of such a pair and of another
+    float *part_dw, *part_dx;                 // split: fp32 partial sums [piece][2 F][D], [piece][T][D]
 };
 
 enum PairKind { kPairForward = 0, kPairSave = 1, kPairRecompute = 2, kPairGrads = 3 };
 
 // One output tile: rows m0 .. m0 + 255 of the pair, columns n0 .. n0 + width - 1 (gate/up:
 // width / 2 outputs; width 256, or 128 for a halved tile), `which` the matrix of a weight
-// gradient (0 gate, 1 up; -1 dx).
+// gradient (0 gate, 1 up; -1 dx).  With K split it is one piece of a tile.
 struct PairTile {
     int m0, n0, width, kblocks, which;
+    int k0, part;      // gradients: first K-block, and which piece of K
 };
 
 // The j-th tile of a pair; false past its last.
@@ -95,27 +98,40 @@ __device__ __forceinline__ bool pair_tile(const PairArgs &p, long long pair, lon
         r.width = half ? 128 : 256;
         r.kblocks = (p.D + 63) / 64;
         r.which = -1;
+        r.k0 = r.part = 0;
         return true;
     }
     r.width = p.halved ? 128 : 256;
     const int nd = (p.D + r.width - 1) / r.width, mf = (p.F + kPairM - 1) / kPairM;
     const bool more = pair < p.more;
     const long long dw = p.n_dw / pairs + (more ? 1 : 0);
+    long long t;
+    int k, split;
     if (j < dw) {
-        grouped_tile(pair + j * pairs, 2 * mf, nd, m, n);
+        t = pair + j * pairs;
+        const long long tiles = 2LL * mf * nd;
+        split = p.split_dw;
+        r.part = (int)(t / tiles);
+        grouped_tile(t % tiles, 2 * mf, nd, m, n);
         r.which = m >= mf;
         r.m0 = (m - (r.which ? mf : 0)) * kPairM;
-        r.kblocks = (p.T + 63) / 64;
+        k = (p.T + 63) / 64;
     } else {
-        const long long k = j - dw, split = p.more * p.dx_more;
-        const long long t = more ? pair + k * p.more : split + (pair - p.more) + k * (pairs - p.more);
-        if (k >= (more ? p.dx_more : p.dx_rest) || t >= p.n_dx) return false;
-        grouped_tile(t, (p.T + kPairM - 1) / kPairM, nd, m, n);
+        const long long i = j - dw, cut = p.more * p.dx_more;
+        t = more ? pair + i * p.more : cut + (pair - p.more) + i * (pairs - p.more);
+        if (i >= (more ? p.dx_more : p.dx_rest) || t >= p.n_dx) return false;
+        const int mt = (p.T + kPairM - 1) / kPairM;
+        const long long tiles = (long long)mt * nd;
+        split = p.split_dx;
+        r.part = (int)(t / tiles);
+        grouped_tile(t % tiles, mt, nd, m, n);
         r.which = -1;
         r.m0 = m * kPairM;
-        r.kblocks = 2 * ((p.F + 63) / 64);
+        k = 2 * ((p.F + 63) / 64);
     }
     r.n0 = n * r.width;
+    r.k0 = (int)((long long)k * r.part / split);
+    r.kblocks = (int)((long long)k * (r.part + 1) / split) - r.k0;
     return true;
 }
 
@@ -142,11 +158,27 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs &p, const PairTile 
         __nv_bfloat16 *out = t.which < 0 ? p.dx : (t.which ? p.dwu : p.dwg);
         const int rows = (t.which < 0 ? p.T : p.F) - r0;
         const int cols = t.width / 2;
+        float *part = t.which < 0 ? p.part_dx : p.part_dw;     // null: K is not split
+        if (part)
+            part += (t.which < 0 ? (size_t)t.part * p.T + r0 : ((size_t)t.part * 2 + t.which) * p.F + r0) * p.D;
 #pragma unroll 1
         for (int c = cols * w; c < cols * w + cols; c += 64) {
             tmem_ld32(taddr + c, a);
             tmem_ld32(taddr + c + 32, b);
             tmem_ld_wait();
+            if (part) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        o[i] = half ? make_uint4(b[4 * i], b[4 * i + 1], b[4 * i + 2], b[4 * i + 3])
+                                    : make_uint4(a[4 * i], a[4 * i + 1], a[4 * i + 2], a[4 * i + 3]);
+                    const int col = t.n0 + c + 32 * half;
+                    warp_store_rows<4>(stage, lane, o, reinterpret_cast<char *>(part + col), (size_t)p.D * 4, rows,
+                                       (p.D - col) * 4, true);
+                }
+                continue;
+            }
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(a[i]);
             pack_row32(v, false, o);
@@ -297,7 +329,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 const int nb = tl.n0 + (tl.width / 2) * rank;
                 const uint32_t bytes = 2 * (kPairStageBytes + (two ? kPairStageBytes : kPairStageBytes / 2));
                 const int half = (args.F + 63) / 64;      // dx: K-blocks of dg, then of du
-                for (int kb = 0; kb < tl.kblocks; ++kb, ++it) {
+                for (int kb = tl.k0; kb < tl.k0 + tl.kblocks; ++kb, ++it) {
                     const int s = it % kPairStages;
                     if (it >= kPairStages && !wait(&sm.empty[s], (it / kPairStages - 1) & 1)) {
                         ok = false;
@@ -383,6 +415,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
 }
 
+// Partial sums of gradients whose K was split, added in the pieces' order and rounded once: 8
+// values a thread.  Memory-bound.
+__global__ void __launch_bounds__(256) grads_reduce_kernel(const PairArgs p) {
+    chain_entry();
+    const long long nw = p.part_dw ? 2LL * p.F * p.D : 0, nx = p.part_dx ? (long long)p.T * p.D : 0;
+    for (long long i = (blockIdx.x * 256LL + threadIdx.x) * 8; i < nw + nx; i += gridDim.x * 2048LL) {
+        const bool w = i < nw;
+        const long long at = w ? i : i - nw, n = w ? nw : nx;
+        const float *src = (w ? p.part_dw : p.part_dx) + at;
+        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        const int pieces = w ? p.split_dw : p.split_dx;
+#pragma unroll 4
+        for (int k = 0; k < pieces; ++k) {
+            float t[8];
+            load8<float>(src + k * n, t);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] += t[j];
+        }
+        const long long fd = (long long)p.F * p.D;
+        __nv_bfloat16 *out = w ? (at < fd ? p.dwg + at : p.dwu + (at - fd)) : p.dx + at;
+        *reinterpret_cast<uint4 *>(out) =
+            make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    }
+}
+
 // What the gradients' products read, from the 8-bit activations, in one launch: the first
 // blocks write x as bf16 (exact for scales that fp8_block_quantize made, down to bf16's least
 // subnormal), the others dg and du.  Both take two rows of 512 columns a warp, as the 8-bit
@@ -450,6 +507,13 @@ __global__ void __launch_bounds__(kStoreWarps * 32) swiglu_saved_kernel(const Sa
 
 // ------------------------------------------------------------------------------ host side
 
+static inline size_t align256_d(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// Estimated times of plan_grads in us: a K-block of 64 in a whole and a halved tile (whose MMAs take
+// half as long; the copies' latency is the same), a piece's start and end, the launch that adds
+// partial sums, and the bytes it moves in one.
+constexpr double kBlockUs = 0.35, kHalfBlockUs = 0.30, kPieceUs = 1.0, kReduceUs = 3.0, kReduceBytesUs = 4e6;
+
 static int pair_map(CUtensorMap *m, const void *base, long long rows, long long cols, int f16) {
     return matrix_map(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, rows, cols,
                       64);
@@ -468,48 +532,73 @@ static long long plan_gateup(PairArgs &p, long long pairs, bool may_halve) {
 }
 
 // Gradient tiles: the dw tiles go round the pairs first; the dx tiles then fill up, so that
-// the most loaded pair has least.  All tiles are halved where that ends sooner (few tiles).
-static long long plan_grads(PairArgs &p, long long pairs) {
+// the most loaded pair has least.  Where there are few tiles they are halved in width, and K of
+// either kind is split (dw: many tokens and a small weight; dx: few tokens and a large one): the
+// pieces' fp32 sums are then added by one more launch.  The choice is the least of the estimated
+// times.  Whole backward pass, GPU us, as chosen and in one whole piece a tile: 8192 tokens, 512 -> 256
+// 26 (dw in 8 pieces), 56; 64 tokens, 4096 -> 4096 59 (dx in 4), 85; 512 tokens, 2048 -> 2048 41 (dx in
+// 4), 48; 1111 tokens, 1000 -> 504 22 (halved), 24.
+static void plan_grads(PairArgs &p, long long pairs) {
     const long long mf = ((long long)p.F + kPairM - 1) / kPairM, mt = ((long long)p.T + kPairM - 1) / kPairM;
     const long long k_dw = ((long long)p.T + 63) / 64, k_dx = 2 * (((long long)p.F + 63) / 64);
-    double best = 0;
+    double best = -1;
     for (int halved = 0; halved < 2; ++halved) {
         const long long width = halved ? 128 : 256, nd = (p.D + width - 1) / width;
-        const long long n_dw = 2 * mf * nd, n_dx = mt * nd;
-        const long long on = n_dw + n_dx < pairs ? n_dw + n_dx : pairs;      // pairs at work
-        const long long q = n_dw / on, more = n_dw % on, rest = on - more;
-        // dx tiles of a pair with q + 1 dw tiles: a, of the others: b
-        long long a = 0, b = 0, load = -1;
-        for (long long x = 0; x <= (more ? (n_dx + more - 1) / more : 0); ++x) {
-            const long long left = n_dx - more * x, y = left > 0 ? (left + rest - 1) / rest : 0;
-            const long long l1 = more ? (q + 1) * k_dw + x * k_dx : 0, l0 = q * k_dw + y * k_dx, l = l1 > l0 ? l1 : l0;
-            if (load < 0 || l < load) {
-                load = l;
-                a = x;
-                b = y;
+        const double t_kb = halved ? kHalfBlockUs : kBlockUs;
+        for (int s_dw = 1; s_dw <= 16 && (s_dw == 1 || s_dw * 4 <= k_dw); s_dw *= 2)
+            for (int s_dx = 1; s_dx <= 16 && (s_dx == 1 || s_dx * 4 <= k_dx); s_dx *= 2) {
+                const long long n_dw = 2 * mf * nd * s_dw, n_dx = mt * nd * s_dx;
+                // a split is for few tiles: no more pieces than pairs
+                if ((s_dw > 1 && n_dw > pairs) || (s_dx > 1 && n_dx > 2 * pairs)) continue;
+                const double u_dw = (double)((k_dw + s_dw - 1) / s_dw) * t_kb + kPieceUs;
+                const double u_dx = (double)((k_dx + s_dx - 1) / s_dx) * t_kb + kPieceUs;
+                const long long on = n_dw + n_dx < pairs ? n_dw + n_dx : pairs;      // pairs at work
+                const long long q = n_dw / on, more = n_dw % on, rest = on - more;
+                // dx pieces of a pair with q + 1 dw pieces: a, of the others: b.  Level loads are
+                // at a = (n_dx u_dx / rest - u_dw) / (u_dx (1 + more / rest)); whole numbers next to it.
+                long long a = 0, b = 0;
+                double load = -1;
+                const double level = (n_dx * u_dx / rest - u_dw) / (u_dx * (1.0 + (double)more / rest));
+                const long long top = more ? (n_dx + more - 1) / more : 0, x0 = level > 1 ? (long long)level - 1 : 0;
+                for (long long x = x0 < top ? x0 : top; x <= top && x <= x0 + 3; ++x) {
+                    const long long left = n_dx - more * x, y = left > 0 ? (left + rest - 1) / rest : 0;
+                    const double l1 = more ? (q + 1) * u_dw + x * u_dx : 0, l0 = q * u_dw + y * u_dx;
+                    const double l = l1 > l0 ? l1 : l0;
+                    if (load < 0 || l < load) {
+                        load = l;
+                        a = x;
+                        b = y;
+                    }
+                }
+                double cost = load;
+                const double sums = (s_dw > 1 ? 2.0 * s_dw * p.F * p.D : 0) + (s_dx > 1 ? 1.0 * s_dx * p.T * p.D : 0);
+                if (sums > 0) cost += kReduceUs + 8 * sums / kReduceBytesUs;
+                if (best < 0 || cost < best) {
+                    best = cost;
+                    p.halved = halved;
+                    p.split_dw = s_dw;
+                    p.split_dx = s_dx;
+                    p.n_dw = n_dw;
+                    p.n_dx = n_dx;
+                    p.more = (int)more;
+                    p.dx_more = a;
+                    p.dx_rest = b;
+                }
             }
-            if (left <= 0) break;
-        }
-        // a halved tile takes a little more than half of a whole one's time: A is read as often
-        const double cost = (double)load * (halved ? 0.6 : 1.0);
-        if (!halved || cost < best) {
-            best = cost;
-            p.halved = halved;
-            p.n_dw = n_dw;
-            p.n_dx = n_dx;
-            p.more = (int)more;
-            p.dx_more = a;
-            p.dx_rest = b;
-        }
     }
-    return p.n_dw + p.n_dx;
+}
+
+// fp32 partial sums of the plan.
+static size_t grads_part_bytes(const PairArgs &p, bool dx) {
+    if (dx) return p.split_dx > 1 ? align256_d((size_t)p.split_dx * p.T * p.D * 4) : 0;
+    return p.split_dw > 1 ? align256_d((size_t)p.split_dw * 2 * p.F * p.D * 4) : 0;
 }
 
 template <int KIND>
 static int launch_pair(const PairMaps &maps, PairArgs p, cudaStream_t s, int stage) {
     const int smem = (int)sizeof(PairSmem) + 1024;
     const long long pairs = num_sms() / 2;
-    const long long tiles = KIND == kPairGrads ? plan_grads(p, pairs) : plan_gateup(p, pairs, KIND != kPairSave);
+    const long long tiles = KIND == kPairGrads ? p.n_dw + p.n_dx : plan_gateup(p, pairs, KIND != kPairSave);
     const unsigned grid = 2 * (unsigned)(tiles < pairs ? tiles : pairs);
     LaunchScope ls(s, stage);
     if (launch_chained(pair_gemm_kernel<KIND>, dim3(grid), dim3(kPairThreads), smem, s, maps, p) != cudaSuccess)
@@ -526,13 +615,11 @@ static int configure_swiglu() {
     if (set_smem(pair_gemm_kernel<kPairForward>, smem) || set_smem(pair_gemm_kernel<kPairSave>, smem) ||
         set_smem(pair_gemm_kernel<kPairRecompute>, smem) || set_smem(pair_gemm_kernel<kPairGrads>, smem) ||
         configure_rows<16, kSwiglu>() || configure_rows<32, kSwiglu>() || configure_rows<64, kSwiglu>() ||
-        configure_rows<128, kSwiglu>() || set_smem(swiglu_saved_kernel, 0) || configure_store())
+        configure_rows<128, kSwiglu>() || set_smem(swiglu_saved_kernel, 0) || set_smem(grads_reduce_kernel, 0) || configure_store())
         return record_cuda_error("configure_swiglu");
     configured.set();
     return TQ_OK;
 }
-
-static inline size_t align256_d(size_t n) { return (n + 255) & ~(size_t)255; }
 
 static int swiglu_shape_status(int T, int D, int F) {
     if (T < 0 || D < 1 || F < 1 || D % 8 || F % 8) return TQ_ERR_INVALID_ARG;
@@ -619,9 +706,22 @@ TQ_API int swiglu_forward(const void *x, const void *w_gate, const void *w_up, i
     return launch_pair<kPairSave>(maps, p, s, kStageSwiglu);
 }
 
+namespace tq {
+// Workspace of a backward call whose plan p holds: dg, du, x as bf16 (from_saved), partial sums.
+static size_t backward_bytes(const PairArgs &p, bool from_saved) {
+    return 2 * align256_d((size_t)p.T * p.F * 2) + (from_saved ? align256_d((size_t)p.T * p.D * 2) : 0) +
+           grads_part_bytes(p, false) + grads_part_bytes(p, true);
+}
+}  // namespace tq
+
 TQ_API size_t swiglu_backward_workspace_size(int T, int D, int F, int from_saved) {
-    if (tq::swiglu_shape_status(T, D, F)) return 0;
-    return 2 * tq::align256_d((size_t)T * F * 2) + (from_saved ? tq::align256_d((size_t)T * D * 2) : 0);
+    if (tq::swiglu_shape_status(T, D, F) || T == 0) return 0;
+    tq::PairArgs p{};
+    p.T = T;
+    p.D = D;
+    p.F = F;
+    tq::plan_grads(p, tq::num_sms() / 2);
+    return tq::backward_bytes(p, from_saved != 0);
 }
 
 TQ_API int swiglu_backward(const void *dh, const void *x, const tq_swiglu_saved *saved, const void *w_gate,
@@ -646,14 +746,15 @@ TQ_API int swiglu_backward(const void *dh, const void *x, const tq_swiglu_saved 
     if (!aligned16(dh) || !aligned16(w_gate) || !aligned16(w_up) || !aligned16(dx) || (x && !aligned16(x)) ||
         (saved && !saved_aligned(saved)) || (ws && !aligned16(ws)))
         return TQ_ERR_ALIGNMENT;
-    if (!ws || ws_bytes < swiglu_backward_workspace_size(T, D, F, saved != nullptr)) return TQ_ERR_WORKSPACE;
-
-    if ((st = configure_swiglu())) return st;
-    char *w = reinterpret_cast<char *>(ws);
     PairArgs p{};
     p.T = T;
     p.D = D;
     p.F = F;
+    plan_grads(p, num_sms() / 2);
+    if (!ws || ws_bytes < backward_bytes(p, saved != nullptr)) return TQ_ERR_WORKSPACE;
+
+    if ((st = configure_swiglu())) return st;
+    char *w = reinterpret_cast<char *>(ws);
     p.dh = reinterpret_cast<const __nv_bfloat16 *>(dh);
     p.dg = reinterpret_cast<__nv_bfloat16 *>(w);
     w += align256_d((size_t)T * F * 2);
@@ -668,6 +769,11 @@ TQ_API int swiglu_backward(const void *dh, const void *x, const tq_swiglu_saved 
     if (!st) st = pair_map(&maps.b1, w_up, F, D, 0);
     if (st) return st;
     const void *xb = x;
+    void *x_bf16 = w;
+    if (saved) w += align256_d((size_t)T * D * 2);
+    if (p.split_dw > 1) p.part_dw = reinterpret_cast<float *>(w);
+    w += grads_part_bytes(p, false);
+    if (p.split_dx > 1) p.part_dx = reinterpret_cast<float *>(w);
     if (saved) {
         SavedArgs a{};
         a.x8 = saved->x;
@@ -677,7 +783,7 @@ TQ_API int swiglu_backward(const void *dh, const void *x, const tq_swiglu_saved 
         a.sg = saved->s_g;
         a.su = saved->s_u;
         a.dh = p.dh;
-        a.x = reinterpret_cast<__nv_bfloat16 *>(w);
+        a.x = reinterpret_cast<__nv_bfloat16 *>(x_bf16);
         a.dg = p.dg;
         a.du = p.du;
         a.T = T;
@@ -688,7 +794,7 @@ TQ_API int swiglu_backward(const void *dh, const void *x, const tq_swiglu_saved 
         a.x_blocks = (long long)gx.x * gx.y;
         const long long blocks = a.x_blocks + (long long)gf.x * gf.y;
         if (blocks > 0x7FFFFFFFLL) return TQ_ERR_UNSUPPORTED;
-        xb = w;
+        xb = x_bf16;
         LaunchScope ls(s, kStageSwigluGrad);
         if (launch_chained(swiglu_saved_kernel, dim3((unsigned)blocks), dim3(kStoreWarps * 32), 0, s, a) != cudaSuccess)
             return record_cuda_error("swiglu_saved_kernel");
@@ -701,6 +807,13 @@ TQ_API int swiglu_backward(const void *dh, const void *x, const tq_swiglu_saved 
     st = pair_map(&maps.a0, p.dg, T, F, 0);
     if (!st) st = pair_map(&maps.a1, p.du, T, F, 0);
     if (!st) st = pair_map(&maps.x, xb, T, D, 0);
-    if (st) return st;
-    return launch_pair<kPairGrads>(maps, p, s, kStageSwigluGrad);
+    if (!st) st = launch_pair<kPairGrads>(maps, p, s, kStageSwigluGrad);
+    if (st || (!p.part_dw && !p.part_dx)) return st;
+    const long long n = (p.part_dw ? 2LL * F * D : 0) + (p.part_dx ? (long long)T * D : 0);
+    const long long blocks = (n / 8 + 255) / 256, most = 8LL * num_sms();
+    LaunchScope ls(s, kStageSwigluGrad);
+    if (launch_chained(grads_reduce_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, s, p) !=
+        cudaSuccess)
+        return record_cuda_error("grads_reduce_kernel");
+    return launch_status();
 }
