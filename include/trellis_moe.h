@@ -367,7 +367,8 @@ typedef struct {
  * swiglu_forward -- h = silu(g) * u with g = x W_gate^T, u = x W_up^T, in one kernel (fp32
  * sums; g and u are not rounded, h once).
  *   x : [T][D], w_gate, w_up : [F][D], h : [T][F], all of dtype (F16 or BF16), 16-byte
- *   aligned.  D % 8 == 0, F % 8 == 0 (each size up to 2^31 - 1024).  Outputs overlap no input.
+ *   aligned.  D % 8 == 0, F % 8 == 0 (each size up to 2^31 - 1024).  Outputs overlap no input and not
+ *   each other.
  *   saved: NULL, or the arrays that receive x, g and u in 8 bits (g and u are stored from
  *   their fp32 sums by the same kernel); h is the same either way up to the order of its sums.
  */
@@ -381,7 +382,8 @@ int swiglu_forward(const void *x, const void *w_gate, const void *w_up, int dtyp
  * from exactly one of x (g and u are computed again) and saved (x, g and u are the 8-bit
  * values that swiglu_forward stored; dx, dw follow from those values).  The other is NULL.
  * dg and du are rounded to bf16 for the products; sums are fp32.  Results are written (not
- * added), do not depend on the order of execution, and must not overlap the inputs.
+ * added), do not depend on the order of execution, and must not overlap the inputs or each
+ * other.
  *   dtype: BF16 (F16: TQ_ERR_UNSUPPORTED, its range does not hold dg and du).
  *   dx : [T][D], dw_gate, dw_up : [F][D].  ws: device workspace of
  *   swiglu_backward_workspace_size(T, D, F, saved != NULL) bytes, 16-byte aligned (the size
