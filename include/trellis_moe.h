@@ -381,7 +381,8 @@ int swiglu_forward(const void *x, const void *w_gate, const void *w_up, int dtyp
  *   dx = dg W_gate + du W_up,  dw_gate = dg^T x,  dw_up = du^T x
  * from exactly one of x (g and u are computed again) and saved (x, g and u are the 8-bit
  * values that swiglu_forward stored; dx, dw follow from those values).  The other is NULL.
- * dg and du are rounded to bf16 for the products; sums are fp32.  Results are written (not
+ * dg and du are rounded to bf16 for the products (for the weight gradients of small problems, T D F
+ * <= 2^29, to two bf16 words); sums are fp32.  Results are written (not
  * added), do not depend on the order of execution, and must not overlap the inputs or each
  * other.
  *   dtype: BF16 (F16: TQ_ERR_UNSUPPORTED, its range does not hold dg and du).

@@ -20,7 +20,11 @@
 // dg and du are rounded to bf16 between the two launches, because the tensor cores take 16-bit
 // operands: at most 2^-8 of each term, and as the terms' errors are independent about as much
 // of a sum as the rounding of the 16-bit gradient itself (measured against 64 bits: 0.0024 of
-// the gradients' norm, 0.0017 for the last rounding alone).
+// the gradients' norm, 0.0017 for the last rounding alone).  For the weight gradients, which a
+// training run adds up, small problems (kTwoWordsMost) keep the remainder as a second bf16 word
+// that K then runs over too, and are left with the last rounding; their products are shorter
+// than the call (777 tokens, 1032 -> 392: a step of 40 us either way).  At 8192 tokens, 4096 -> 1024 the
+// second word would add 100 us to 300.
 //
 // Few tokens: dense_rows_kernel (weights streamed once, tokens on the MMA's N side).
 #include "tq_dense_rows.cuh"
@@ -49,6 +53,7 @@ static_assert(sizeof(PairSmem) + 1024 <= 227 * 1024, "pair GEMM shared memory");
 // Every map reads boxes of 64 x 64 elements.
 struct PairMaps {
     CUtensorMap a0, a1, b0, b1, x;
+    CUtensorMap a0_lo, a1_lo;     // weight gradients in two words: the second words of dg and du
 };
 
 struct PairArgs {
@@ -59,6 +64,8 @@ struct PairArgs {
     float *sg, *su;                           // [T][ceil(F / 128)]
     const __nv_bfloat16 *dh;                  // [T][F]
     __nv_bfloat16 *dg, *du;                   // [T][F]
+    __nv_bfloat16 *dg_lo, *du_lo;             // [T][F], two words
+    int words;                                // of dg and du: 1, 2
     __nv_bfloat16 *dx, *dwg, *dwu;            // [T][D], [F][D], [F][D]
     // tile plan (plan_gateup, plan_grads)
     long long full;                           // gate/up: whole tiles; the others are halved
@@ -71,7 +78,9 @@ struct PairArgs {
     float *part_dw, *part_dx;                 // split: fp32 partial sums [piece][2 F][D], [piece][T][D]
 };
 
-enum PairKind { kPairForward = 0, kPairSave = 1, kPairRecompute = 2, kPairGrads = 3 };
+// kPairRecompute and kPairRecomputeTwo: dg and du in one word and in two (a kernel of its own, since
+// the second word's code costs the first word's registers).
+enum PairKind { kPairForward = 0, kPairSave = 1, kPairRecompute = 2, kPairGrads = 3, kPairRecomputeTwo = 4 };
 
 // One output tile: rows m0 .. m0 + 255 of the pair, columns n0 .. n0 + width - 1 (gate/up:
 // width / 2 outputs; width 256, or 128 for a halved tile), `which` the matrix of a weight
@@ -115,7 +124,7 @@ __device__ __forceinline__ bool pair_tile(const PairArgs &p, long long pair, lon
         grouped_tile(t % tiles, 2 * mf, nd, m, n);
         r.which = m >= mf;
         r.m0 = (m - (r.which ? mf : 0)) * kPairM;
-        k = (p.T + 63) / 64;
+        k = p.words * ((p.T + 63) / 64);
     } else {
         const long long i = j - dw, cut = p.more * p.dx_more;
         t = more ? pair + i * p.more : cut + (pair - p.more) + i * (pairs - p.more);
@@ -143,6 +152,71 @@ __device__ __forceinline__ void pack_row32(const float (&v)[32], bool f16, uint4
     for (int j = 0; j < 4; ++j)
         p[j] = make_uint4(pack16(v[8 * j], v[8 * j + 1], f16), pack16(v[8 * j + 2], v[8 * j + 3], f16),
                           pack16(v[8 * j + 4], v[8 * j + 5], f16), pack16(v[8 * j + 6], v[8 * j + 7], f16));
+}
+
+// What rounding a value to bf16 leaves; 0 where that is no number (the first word says it then).
+__device__ __forceinline__ float bf16_remainder(float v) {
+    const float d = v - __bfloat162float(__float2bfloat16_rn(v));
+    return fabsf(d) <= FLT_MAX ? d : 0.f;
+}
+
+// The h tile (WORD < 0), or word WORD of the dg and du tiles, of one warp: columns c0 .. c0 + 63 of
+// its rows, or 32 of a halved tile (the second half of o is then not stored).
+template <int WORD>
+__device__ __forceinline__ void store_outputs(const PairArgs &p, const PairTile &t, uint32_t taddr, int r0, int lane,
+                                              int w, unsigned char *stage) {
+    uint32_t a[32], b[32];
+    float v[32];
+    uint4 o[8], o2[8];
+    const bool halved = t.width != 256;
+    const int c0 = (halved ? 32 : 64) * w, u0 = t.width / 2;
+    const int r = r0 + lane, rows = p.T - r0;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        if (half && halved) break;
+        const int c = c0 + 32 * half;
+        tmem_ld32(taddr + c, a);
+        tmem_ld32(taddr + u0 + c, b);
+        const int col = t.n0 + c;
+        if constexpr (WORD >= 0) {
+            uint4 d[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                d[j] = r < p.T && col + 8 * j < p.F
+                           ? __ldg(reinterpret_cast<const uint4 *>(p.dh + (size_t)r * p.F + col + 8 * j))
+                           : make_uint4(0, 0, 0, 0);
+            tmem_ld_wait();
+            float du[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const uint32_t w2 = reinterpret_cast<const uint32_t *>(d)[i >> 1];
+                const float dh = __uint_as_float((i & 1) ? (w2 & 0xFFFF0000u) : (w2 << 16));
+                swiglu_grads(__uint_as_float(a[i]), __uint_as_float(b[i]), dh, v[i], du[i]);
+                if (WORD == 1) {
+                    v[i] = bf16_remainder(v[i]);
+                    du[i] = bf16_remainder(du[i]);
+                }
+            }
+            pack_row32(v, false, o + 4 * half);
+            pack_row32(du, false, o2 + 4 * half);
+        } else {
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = swiglu_value(__uint_as_float(a[i]), __uint_as_float(b[i]));
+            pack_row32(v, p.f16 != 0, o + 4 * half);
+        }
+    }
+    const int col = t.n0 + c0;
+    const int bytes = min((p.F - col) * 2, halved ? 64 : 128);
+    const size_t at = (size_t)r0 * p.F + col;
+    if constexpr (WORD >= 0) {
+        warp_store_rows<2>(stage, lane, o, reinterpret_cast<char *>((WORD == 1 ? p.dg_lo : p.dg) + at), (size_t)p.F * 2, rows,
+                           bytes, true);
+        warp_store_rows<2>(stage, lane, o2, reinterpret_cast<char *>((WORD == 1 ? p.du_lo : p.du) + at), (size_t)p.F * 2, rows,
+                           bytes, true);
+    } else {
+        warp_store_rows<2>(stage, lane, o, reinterpret_cast<char *>(p.h) + at * 2, (size_t)p.F * 2, rows, bytes, true);
+    }
 }
 
 // One warp's share of a tile: rows row0 .. row0 + 31 of the tile (tensor-memory lane quarter
@@ -227,50 +301,8 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs &p, const PairTile 
         warp_store_rows<2>(stage, lane, o, reinterpret_cast<char *>((w ? p.u8 : p.g8) + (size_t)r0 * p.F + t.n0),
                            (size_t)p.F, rows, p.F - t.n0, p.F % 16 == 0);
     }
-    uint4 o2[8];     // du (backward)
-    // the warp's columns: 64, or 32 of a halved tile (the second half of o is then not stored)
-    const bool halved = t.width != 256;
-    const int c0 = (halved ? 32 : 64) * w, u0 = t.width / 2;
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        if (half && halved) break;
-        const int c = c0 + 32 * half;
-        tmem_ld32(taddr + c, a);
-        tmem_ld32(taddr + u0 + c, b);
-        const int col = t.n0 + c;
-        if constexpr (KIND == kPairRecompute) {
-            uint4 d[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                d[j] = r < p.T && col + 8 * j < p.F
-                           ? __ldg(reinterpret_cast<const uint4 *>(p.dh + (size_t)r * p.F + col + 8 * j))
-                           : make_uint4(0, 0, 0, 0);
-            tmem_ld_wait();
-            float du[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const uint32_t w2 = reinterpret_cast<const uint32_t *>(d)[i >> 1];
-                const float dh = __uint_as_float((i & 1) ? (w2 & 0xFFFF0000u) : (w2 << 16));
-                swiglu_grads(__uint_as_float(a[i]), __uint_as_float(b[i]), dh, v[i], du[i]);
-            }
-            pack_row32(v, false, o + 4 * half);
-            pack_row32(du, false, o2 + 4 * half);
-        } else {
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = swiglu_value(__uint_as_float(a[i]), __uint_as_float(b[i]));
-            pack_row32(v, p.f16 != 0, o + 4 * half);
-        }
-    }
-    const int col = t.n0 + c0;
-    const int bytes = min((p.F - col) * 2, halved ? 64 : 128);
-    const size_t at = (size_t)r0 * p.F + col;
-    if constexpr (KIND == kPairRecompute) {
-        warp_store_rows<2>(stage, lane, o, reinterpret_cast<char *>(p.dg + at), (size_t)p.F * 2, rows, bytes, true);
-        warp_store_rows<2>(stage, lane, o2, reinterpret_cast<char *>(p.du + at), (size_t)p.F * 2, rows, bytes, true);
-    } else {
-        warp_store_rows<2>(stage, lane, o, reinterpret_cast<char *>(p.h) + at * 2, (size_t)p.F * 2, rows, bytes, true);
-    }
+    store_outputs<KIND == kPairRecompute || KIND == kPairRecomputeTwo ? 0 : -1>(p, t, taddr, r0, lane, w, stage);
+    if constexpr (KIND == kPairRecomputeTwo) store_outputs<1>(p, t, taddr, r0, lane, w, stage);
 }
 
 // ------------------------------------------------------------------------------ kernel
@@ -328,7 +360,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 const bool two = tl.width == 256;         // B rows of a CTA: 128, or 64
                 const int nb = tl.n0 + (tl.width / 2) * rank;
                 const uint32_t bytes = 2 * (kPairStageBytes + (two ? kPairStageBytes : kPairStageBytes / 2));
-                const int half = (args.F + 63) / 64;      // dx: K-blocks of dg, then of du
+                // dx: K-blocks of dg, then of du; dw: of the tokens, then again for the second word
+                const int half = (args.F + 63) / 64, tokens = (args.T + 63) / 64;
                 for (int kb = tl.k0; kb < tl.k0 + tl.kblocks; ++kb, ++it) {
                     const int s = it % kPairStages;
                     if (it >= kPairStages && !wait(&sm.empty[s], (it / kPairStages - 1) & 1)) {
@@ -342,8 +375,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                         load(sm.a[s], &maps.a0, ar, kb * 64, false, true, bar);
                         load(sm.b[s], rank ? &maps.b1 : &maps.b0, tl.n0, kb * 64, false, two, bar);
                     } else if (tl.which >= 0) {
-                        load(sm.a[s], tl.which ? &maps.a1 : &maps.a0, ar, kb * 64, true, true, bar);
-                        load(sm.b[s], &maps.x, nb, kb * 64, true, two, bar);
+                        const bool lo = kb >= tokens;
+                        const int k0 = (lo ? kb - tokens : kb) * 64;
+                        load(sm.a[s], tl.which ? (lo ? &maps.a1_lo : &maps.a1) : (lo ? &maps.a0_lo : &maps.a0), ar, k0,
+                             true, true, bar);
+                        load(sm.b[s], &maps.x, nb, k0, true, two, bar);
                     } else {
                         const bool up = kb >= half;
                         const int k0 = (up ? kb - half : kb) * 64;
@@ -448,7 +484,7 @@ struct SavedArgs {
     const uint8_t *x8, *g8, *u8;
     const float *sx, *sg, *su;
     const __nv_bfloat16 *dh;
-    __nv_bfloat16 *x, *dg, *du;
+    __nv_bfloat16 *x, *dg, *du, *dg_lo, *du_lo;     // second words: null with one
     int T, D, F;
     long long row_blocks, x_blocks;
 };
@@ -502,12 +538,25 @@ __global__ void __launch_bounds__(kStoreWarps * 32) swiglu_saved_kernel(const Sa
                 make_uint4(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(a[4], a[5]), pack_bf16(a[6], a[7]));
             *reinterpret_cast<uint4 *>(p.du + at) =
                 make_uint4(pack_bf16(c[0], c[1]), pack_bf16(c[2], c[3]), pack_bf16(c[4], c[5]), pack_bf16(c[6], c[7]));
+            if (!p.dg_lo) continue;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                a[j] = bf16_remainder(a[j]);
+                c[j] = bf16_remainder(c[j]);
+            }
+            *reinterpret_cast<uint4 *>(p.dg_lo + at) =
+                make_uint4(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(a[4], a[5]), pack_bf16(a[6], a[7]));
+            *reinterpret_cast<uint4 *>(p.du_lo + at) =
+                make_uint4(pack_bf16(c[0], c[1]), pack_bf16(c[2], c[3]), pack_bf16(c[4], c[5]), pack_bf16(c[6], c[7]));
         }
 }
 
 // ------------------------------------------------------------------------------ host side
 
 static inline size_t align256_d(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// T D F up to which the weight gradients take dg and du in two bf16 words.
+constexpr double kTwoWordsMost = 512.0 * 1024 * 1024;
 
 // Estimated times of plan_grads in us: a K-block of 64 in a whole and a halved tile (whose MMAs take
 // half as long; the copies' latency is the same), a piece's start and end, the launch that adds
@@ -540,7 +589,8 @@ static long long plan_gateup(PairArgs &p, long long pairs, bool may_halve) {
 // 4), 48; 1111 tokens, 1000 -> 504 22 (halved), 24.
 static void plan_grads(PairArgs &p, long long pairs) {
     const long long mf = ((long long)p.F + kPairM - 1) / kPairM, mt = ((long long)p.T + kPairM - 1) / kPairM;
-    const long long k_dw = ((long long)p.T + 63) / 64, k_dx = 2 * (((long long)p.F + 63) / 64);
+    p.words = (double)p.T * p.D * p.F <= kTwoWordsMost ? 2 : 1;
+    const long long k_dw = p.words * (((long long)p.T + 63) / 64), k_dx = 2 * (((long long)p.F + 63) / 64);
     double best = -1;
     for (int halved = 0; halved < 2; ++halved) {
         const long long width = halved ? 128 : 256, nd = (p.D + width - 1) / width;
@@ -613,7 +663,7 @@ static int configure_swiglu() {
     if (configured.get()) return TQ_OK;
     const int smem = (int)sizeof(PairSmem) + 1024;
     if (set_smem(pair_gemm_kernel<kPairForward>, smem) || set_smem(pair_gemm_kernel<kPairSave>, smem) ||
-        set_smem(pair_gemm_kernel<kPairRecompute>, smem) || set_smem(pair_gemm_kernel<kPairGrads>, smem) ||
+        set_smem(pair_gemm_kernel<kPairRecompute>, smem) || set_smem(pair_gemm_kernel<kPairRecomputeTwo>, smem) || set_smem(pair_gemm_kernel<kPairGrads>, smem) ||
         configure_rows<16, kSwiglu>() || configure_rows<32, kSwiglu>() || configure_rows<64, kSwiglu>() ||
         configure_rows<128, kSwiglu>() || set_smem(swiglu_saved_kernel, 0) || set_smem(grads_reduce_kernel, 0) || configure_store())
         return record_cuda_error("configure_swiglu");
@@ -709,7 +759,7 @@ TQ_API int swiglu_forward(const void *x, const void *w_gate, const void *w_up, i
 namespace tq {
 // Workspace of a backward call whose plan p holds: dg, du, x as bf16 (from_saved), partial sums.
 static size_t backward_bytes(const PairArgs &p, bool from_saved) {
-    return 2 * align256_d((size_t)p.T * p.F * 2) + (from_saved ? align256_d((size_t)p.T * p.D * 2) : 0) +
+    return 2 * p.words * align256_d((size_t)p.T * p.F * 2) + (from_saved ? align256_d((size_t)p.T * p.D * 2) : 0) +
            grads_part_bytes(p, false) + grads_part_bytes(p, true);
 }
 }  // namespace tq
@@ -760,6 +810,12 @@ TQ_API int swiglu_backward(const void *dh, const void *x, const tq_swiglu_saved 
     w += align256_d((size_t)T * F * 2);
     p.du = reinterpret_cast<__nv_bfloat16 *>(w);
     w += align256_d((size_t)T * F * 2);
+    if (p.words == 2) {
+        p.dg_lo = reinterpret_cast<__nv_bfloat16 *>(w);
+        w += align256_d((size_t)T * F * 2);
+        p.du_lo = reinterpret_cast<__nv_bfloat16 *>(w);
+        w += align256_d((size_t)T * F * 2);
+    }
     p.dx = reinterpret_cast<__nv_bfloat16 *>(dx);
     p.dwg = reinterpret_cast<__nv_bfloat16 *>(dw_gate);
     p.dwu = reinterpret_cast<__nv_bfloat16 *>(dw_up);
@@ -786,6 +842,8 @@ TQ_API int swiglu_backward(const void *dh, const void *x, const tq_swiglu_saved 
         a.x = reinterpret_cast<__nv_bfloat16 *>(x_bf16);
         a.dg = p.dg;
         a.du = p.du;
+        a.dg_lo = p.dg_lo;
+        a.du_lo = p.du_lo;
         a.T = T;
         a.D = D;
         a.F = F;
@@ -801,12 +859,15 @@ TQ_API int swiglu_backward(const void *dh, const void *x, const tq_swiglu_saved 
     } else {
         st = pair_map(&maps.a0, x, T, D, 0);
         if (st) return st;
-        st = launch_pair<kPairRecompute>(maps, p, s, kStageSwigluGrad);
+        st = p.words == 2 ? launch_pair<kPairRecomputeTwo>(maps, p, s, kStageSwigluGrad)
+                          : launch_pair<kPairRecompute>(maps, p, s, kStageSwigluGrad);
     }
     if (st) return st;
     st = pair_map(&maps.a0, p.dg, T, F, 0);
     if (!st) st = pair_map(&maps.a1, p.du, T, F, 0);
     if (!st) st = pair_map(&maps.x, xb, T, D, 0);
+    if (!st && p.words == 2) st = pair_map(&maps.a0_lo, p.dg_lo, T, F, 0);
+    if (!st && p.words == 2) st = pair_map(&maps.a1_lo, p.du_lo, T, F, 0);
     if (!st) st = launch_pair<kPairGrads>(maps, p, s, kStageSwigluGrad);
     if (st || (!p.part_dw && !p.part_dx)) return st;
     const long long n = (p.part_dw ? 2LL * F * D : 0) + (p.part_dx ? (long long)T * D : 0);
