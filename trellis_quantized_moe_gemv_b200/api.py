@@ -441,8 +441,12 @@ def _require_matrix(t, dtype, name, dev):
     raise ValueError("%s is on %s, but the current device is cuda:%d" % (name, t.device, dev))
 
 
+# The current stream's handle on a device.
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _raw_stream(stream, dev):
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    return _current_stream(dev) if stream is None else stream.cuda_stream
 
 
 def _new(rows, cols, dtype, device, stream):
@@ -621,13 +625,18 @@ def swiglu_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, ou
     """h = silu(x w_gate^T) * (x w_up^T): x [T, D], w_gate and w_up [F, D], all bf16 or all
     fp16, D and F multiples of 8; h [T, F].  `saved` receives x and the two projections in
     8 bits for swiglu_backward."""
-    dt, dev = _float_dtype(x, "x"), _here(x)
-    T, D = _require_matrix(x, x.dtype, "x", dev)
-    F, wd = _swiglu_weights(w_gate, w_up, x.dtype, dev)
+    dt, dev, dtype = _float_dtype(x, "x"), _here(x), x.dtype
+    T, D = _require_matrix(x, dtype, "x", dev)
+    shape = _require_matrix(w_gate, dtype, "w_gate", dev)
+    _require_dense(w_up, dtype, shape, "w_up", dev)
+    F, wd = shape
     if wd != D:
         raise ValueError("w_gate has %d inputs, x has %d" % (wd, D))
     st = None if saved is None else ctypes.byref(saved.struct(T, D, F, dev))
-    out = _out(out, T, F, x.dtype, "out", x, dev, stream)
+    if out is None and stream is None:
+        out = torch.empty(T, F, dtype=dtype, device=x.device)
+    else:
+        out = _out(out, T, F, dtype, "out", x, dev, stream)
     _check(_fn("swiglu_forward")(x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), dt, T, D, F, out.data_ptr(), st,
                                  _raw_stream(stream, dev)), "swiglu_forward")
     return out
