@@ -112,7 +112,8 @@ def test_quantize_writes_nothing_else(api):
 SHAPES = [(1, 1, 16), (1, 128, 128), (2, 7, 112), (16, 129, 144), (17, 256, 384), (33, 1001, 272), (64, 200, 2064),
           (65, 64, 128), (128, 300, 1040), (129, 130, 128), (255, 256, 256), (257, 1000, 400), (520, 513, 1168),
           # the pair kernel: several rounds of tiles, a ragged one in every size
-          (1300, 1500, 272), (257, 9503, 144), (2100, 1030, 1168), (4100, 5000, 48),
+          (1300, 1500, 272), (257, 9503, 144), (2100, 1030, 1168), (4100, 5000, 48), (1500, 1300, 1024),
+          (1500, 1300, 1536), (1100, 2050, 2000),
           # one launch up to 128 blocks of a row, two beyond
           (9, 513, 2048), (16, 200, 1024), (16, 200, 8208), (3, 20000, 2064)]
 
@@ -485,6 +486,41 @@ print("captured", api.device_status())
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "captured 0", r.stdout + r.stderr
+
+
+@pytest.mark.parametrize("T", [8, 150, 1500])
+def test_a_chain_of_calls_on_the_same_buffers_without_waiting(api, T):
+    """Each call reads what the one before it wrote (the launches overlap: a kernel may start
+    before the one before it ends), into the same buffers again and again."""
+    D, F = 256, 136
+    w1, s1 = api.fp8_block_quantize(rand((D, 192), 1, F32, 192 ** -0.5), 128)
+    w2, s2 = api.fp8_block_quantize(rand((F, 192), 2, F32, 192 ** -0.5), 128)
+    a, b = rand((F, D), 3, BF16, D ** -0.5), rand((F, D), 4, BF16, D ** -0.5)
+    ins = [rand((T, 192), 10 + i, BF16) for i in range(6)]
+    e = lambda *n: torch.empty(n, dtype=BF16, device="cuda")
+    x, dh, h, dx, da, db = e(T, D), e(T, F), e(T, F), e(T, D), e(F, D), e(F, D)
+    saved = api.SwigluSaved(T, D, F)
+    ws = torch.empty(max(api.fp8_block_linear_workspace_size(T, max(D, F), 192), 16), dtype=torch.uint8, device="cuda")
+    ws2 = torch.empty(api.swiglu_backward_workspace_size(T, D, F, True), dtype=torch.uint8, device="cuda")
+
+    def step(v, wait):
+        calls = [lambda: api.fp8_block_linear(v, w1, s1, out=x, ws=ws),
+                 lambda: api.fp8_block_linear(v, w2, s2, out=dh, ws=ws),
+                 lambda: api.swiglu_backward(dh, a, b, x=x, dx=dx, dw_gate=da, dw_up=db, ws=ws2),
+                 lambda: api.swiglu_forward(dx, a, b, out=h, saved=saved),
+                 lambda: api.swiglu_backward(h, a, b, saved=saved, dx=dx, dw_gate=da, dw_up=db, ws=ws2)]
+        for f in calls:
+            f()
+            if wait:
+                torch.cuda.synchronize()
+        return [t.clone() for t in (x, dh, h, dx, da, db)]
+
+    want = [step(v, True) for v in ins]
+    for _ in range(5):
+        got = [step(v, False) for v in ins]
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(p, q) for p, q in zip(g, w))
 
 
 def test_on_another_stream(api):

@@ -1,5 +1,9 @@
 // Shared pieces of the dense (not trellis-coded) operators: CTA-pair tcgen05 helpers,
 // cluster helpers, tensor maps of row-major matrices, E4M3 block scaling.
+//
+// The kernels are launched chained (a kernel may start before the one before it has ended, and
+// waits in chain_entry), so what they read may still be written while they start: no pointer is
+// declared __restrict__ and no load goes through the read-only path.
 #pragma once
 
 #include "tq_common.cuh"

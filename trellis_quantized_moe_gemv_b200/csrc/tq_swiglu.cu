@@ -183,7 +183,7 @@ __device__ __forceinline__ void store_outputs(const PairArgs &p, const PairTile 
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 d[j] = r < p.T && col + 8 * j < p.F
-                           ? __ldg(reinterpret_cast<const uint4 *>(p.dh + (size_t)r * p.F + col + 8 * j))
+                           ? *reinterpret_cast<const uint4 *>(p.dh + (size_t)r * p.F + col + 8 * j)
                            : make_uint4(0, 0, 0, 0);
             tmem_ld_wait();
             float du[32];
