@@ -583,13 +583,12 @@ class SwigluSaved:
 
     def __init__(self, T: int, D: int, F: int, device="cuda"):
         self.T, self.D, self.F = T, D, F
-        d, f = _blocks(D), _blocks(F)
-        sizes = (T * D, 4 * T * d, T * F, 4 * T * f, T * F, 4 * T * f)
-        self._at, n = [], 0
-        for size in sizes:
-            self._at.append(n)
-            n += size + 255 & ~255
-        self.buffer = torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+        x, f = T * D + 255 & ~255, T * F + 255 & ~255                       # E4M3 parts
+        s_x, s_f = 4 * T * _blocks(D) + 255 & ~255, 4 * T * _blocks(F) + 255 & ~255
+        g = x + s_x
+        u = g + f + s_f
+        self._at = (0, x, g, g + f, u, u + f)
+        self.buffer = torch.empty(u + f + s_f or 256, dtype=torch.uint8, device=device)
 
     @staticmethod
     def empty(T: int, D: int, F: int, device="cuda") -> "SwigluSaved":
@@ -610,14 +609,8 @@ class SwigluSaved:
         if (self.T, self.D, self.F) != (T, D, F):
             raise ValueError("saved must have the shape T, D, F = %s, got %s" % ((T, D, F), (self.T, self.D, self.F)))
         _require_dense(self.buffer, torch.uint8, self.buffer.shape, "saved", dev)
-        p = self.buffer.data_ptr()
-        return TqSwigluSaved(*[p + at for at in self._at])
-
-
-def _swiglu_weights(w_gate, w_up, dtype, dev):
-    shape = _require_matrix(w_gate, dtype, "w_gate", dev)
-    _require_dense(w_up, dtype, shape, "w_up", dev)
-    return shape
+        p, at = self.buffer.data_ptr(), self._at
+        return TqSwigluSaved(p, p + at[1], p + at[2], p + at[3], p + at[4], p + at[5])
 
 
 def swiglu_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, out: Optional[torch.Tensor] = None,
@@ -656,15 +649,21 @@ def swiglu_backward(dh: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, 
         raise ValueError("swiglu_backward takes exactly one of x and saved")
     dt, dev, dtype = _float_dtype(dh, "dh"), _here(dh), dh.dtype
     T, hf = _require_matrix(dh, dtype, "dh", dev)
-    F, D = _swiglu_weights(w_gate, w_up, dtype, dev)
+    shape = _require_matrix(w_gate, dtype, "w_gate", dev)
+    _require_dense(w_up, dtype, shape, "w_up", dev)
+    F, D = shape
     if hf != F:
         raise ValueError("dh has %d columns, w_gate has %d outputs" % (hf, F))
     if x is not None:
         _require_dense(x, dtype, (T, D), "x", dev)
     st = None if saved is None else ctypes.byref(saved.struct(T, D, F, dev))
-    dx = _out(dx, T, D, dtype, "dx", dh, dev, stream)
-    dw_gate = _out(dw_gate, F, D, dtype, "dw_gate", dh, dev, stream)
-    dw_up = _out(dw_up, F, D, dtype, "dw_up", dh, dev, stream)
+    if dx is None and dw_gate is None and dw_up is None and stream is None:
+        dx = torch.empty(T, D, dtype=dtype, device=dh.device)
+        dw_gate, dw_up = torch.empty_like(w_gate), torch.empty_like(w_up)
+    else:
+        dx = _out(dx, T, D, dtype, "dx", dh, dev, stream)
+        dw_gate = _out(dw_gate, F, D, dtype, "dw_gate", dh, dev, stream)
+        dw_up = _out(dw_up, F, D, dtype, "dw_up", dh, dev, stream)
     ws, ptr, size = _workspace(ws, swiglu_backward_workspace_size(T, D, F, saved is not None), dh, dev, stream)
     _check(_fn("swiglu_backward")(dh.data_ptr(), None if x is None else x.data_ptr(), st, w_gate.data_ptr(),
                                   w_up.data_ptr(), dt, T, D, F, dx.data_ptr(), dw_gate.data_ptr(), dw_up.data_ptr(),
