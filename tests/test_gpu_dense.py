@@ -324,6 +324,65 @@ def test_gradients_of_integers_are_exact(api, T, D, F):
         assert (buf[-1] == 5.0).all()
 
 
+@pytest.mark.parametrize("T,D,F", [(3000, 2048, 2904), (814, 5992, 3416), (2600, 2304, 2600), (8000, 1160, 1032),
+                                   (2050, 4104, 1160)])
+def test_many_tiles(api, T, D, F):
+    """Sizes with several rounds of tiles, some taken two at a time with a last one past the
+    matrix, against the definition in 64 bits (on the GPU); guard rows and scales stay."""
+    x, a, b = swiglu_inputs(T, D, F, 77)
+    dh = rand((T, F), 78, BF16, 0.1)
+    X, A, B, DH = (v.double() for v in (x, a, b, dh))
+    g, u = X @ A.t(), X @ B.t()
+    n = (D + 1) * 2.0 ** -23
+    eg, eu = n * (X.abs() @ A.abs().t()), n * (X.abs() @ B.abs().t())
+    h = g * torch.sigmoid(g) * u
+    tol = 1.1 * (u.abs() + eu) * eg + g.abs() * eu + 2 * FAST * (h.abs() + (u.abs() + g.abs()) * 1.1 * (eg + eu))
+
+    def check(got, want, tol):
+        lim = tol + HALF[BF16] * (want.abs() + tol) + LEAST[BF16]
+        assert bool(((got.double() - want).abs() <= lim).all())
+
+    buf = torch.full((T + 1, F), 3.0, dtype=BF16, device="cuda")
+    check(api.swiglu_forward(x, a, b, out=buf[:T]), h, tol)
+    assert (buf[T] == 3.0).all()
+    saved = api.SwigluSaved(T, D, F)
+    saved.buffer.fill_(0xA5)
+    before = saved.buffer.clone()
+    check(api.swiglu_forward(x, a, b, out=buf[:T], saved=saved), h, tol)
+    assert (buf[T] == 3.0).all()
+    inside = torch.zeros_like(saved.buffer, dtype=torch.bool)      # the parts; between them nothing is written
+    for at, size in zip(saved._at, (T * D, 4 * T * -(-D // 128), T * F, 4 * T * -(-F // 128), T * F, 4 * T * -(-F // 128))):
+        inside[at:at + size] = True
+    assert torch.equal(saved.buffer[~inside], before[~inside])
+    q, s = api.fp8_block_quantize(x)
+    assert torch.equal(saved.x.view(torch.uint8), q.view(torch.uint8)) and torch.equal(saved.s_x, s)
+    vals = []
+    for q, s, want, off in ((saved.g, saved.s_g, g, eg), (saved.u, saved.s_u, u, eu)):
+        sc = s.double().repeat_interleave(128, 1)[:, :F]
+        y = q.double() * sc
+        # half a step of E4M3 at most: 2^-4 of the value, or of the least normal value 2^-6
+        lim = off + 2.0 ** -4 * torch.maximum(want.abs() + off, sc * 2.0 ** -6)
+        assert bool(((y - want).abs() <= lim).all())
+        vals.append(y)
+    sx = saved.s_x.double().repeat_interleave(128, 1)[:, :D]
+    cases = [(dict(x=x), X, g, u, eg, eu), (dict(saved=saved), saved.x.double() * sx, vals[0], vals[1], 0.0, 0.0)]
+    for kw, xv, gv, uv, dg_, du_ in cases:
+        sg = torch.sigmoid(gv)
+        dg, du = DH * uv * sg * (1 + gv * (1 - sg)), DH * gv * sg
+        e1 = DH.abs() * (1.1 * du_ + 0.5 * (uv.abs() + du_) * dg_ + (uv.abs() + du_) * FAST * (1.1 + gv.abs()))
+        e2 = DH.abs() * (1.1 * dg_ + (gv.abs() + dg_) * FAST)
+        e1 = e1 + HALF[BF16] * (dg.abs() + e1) + 2.0 ** -133
+        e2 = e2 + HALF[BF16] * (du.abs() + e2) + 2.0 ** -133
+        m1, m2 = dg.abs() + e1, du.abs() + e2
+        bufs = [torch.full((r + 1, D), 5.0, dtype=BF16, device="cuda") for r in (T, F, F)]
+        got = api.swiglu_backward(dh, a, b, dx=bufs[0][:T], dw_gate=bufs[1][:F], dw_up=bufs[2][:F], **kw)
+        kx, kw_ = (2 * F + 1) * 2.0 ** -23, (T + 1) * 2.0 ** -23
+        check(got[0], dg @ A + du @ B, e1 @ A.abs() + e2 @ B.abs() + kx * (m1 @ A.abs() + m2 @ B.abs()))
+        check(got[1], dg.t() @ xv, e1.t() @ xv.abs() + kw_ * (m1.t() @ xv.abs()))
+        check(got[2], du.t() @ xv, e2.t() @ xv.abs() + kw_ * (m2.t() @ xv.abs()))
+        assert all((v[-1] == 5.0).all() for v in bufs)
+
+
 def test_large_gates_and_nan_rows(api):
     """|g| up to 1e4: e^-g overflows or vanishes; a row with a NaN leaves the others alone."""
     T, D, F = 40, 64, 72

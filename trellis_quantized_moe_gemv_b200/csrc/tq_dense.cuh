@@ -62,6 +62,18 @@ __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_add
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// One look at a barrier, without the wait that a try_wait may take.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // ------------------------------------------------------------------------------ CTA pair
 
 // Tensor copy into this CTA's shared memory whose bytes complete on a barrier of either
@@ -225,9 +237,12 @@ __device__ __forceinline__ uint32_t pack16(float a, float b, bool f16) { return 
 
 // An accumulator thread holds a row, so its own stores would touch 32 rows an instruction
 // and write a 32-byte sector in two to four pieces.  A warp instead passes 32 rows x 128
-// bytes through shared memory (rows 144 bytes apart: no bank conflicts) and stores four
-// whole 128-byte row pieces an instruction.
-constexpr int kRowStage = 32 * 144;      // bytes a warp
+// bytes through shared memory (16-byte chunk i of row r at chunk i ^ (r mod 8): no bank conflicts)
+// and stores four whole 128-byte row pieces an instruction.
+constexpr int kRowStage = 32 * 128;      // bytes a warp
+
+// Place of byte c of row r in a warp's stage.
+__device__ __forceinline__ int row_stage_at(int r, int c) { return r * 128 + ((((c >> 4) ^ r) & 7) << 4) + (c & 15); }
 
 // v: the lane's row (row `lane` of 32, 128 bytes); out: the warp's first row at its first
 // byte; row_bytes: distance of rows; rows, bytes: how many of the 32 rows and 128 bytes exist.
@@ -238,7 +253,7 @@ __device__ __forceinline__ void warp_store_rows(unsigned char *stage, int lane, 
                                                 size_t row_bytes, int rows, int bytes, bool vec16,
                                                 bool accumulate = false) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4 *>(stage + lane * 144 + 16 * i) = v[i];
+    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4 *>(stage + row_stage_at(lane, 16 * i)) = v[i];
     __syncwarp();
     if (vec16) {
         const int c = (lane & 7) * 16;
@@ -246,7 +261,7 @@ __device__ __forceinline__ void warp_store_rows(unsigned char *stage, int lane, 
         for (int i = 0; i < 8; ++i) {
             const int r = 4 * i + (lane >> 3);
             if (r < rows && c < bytes) {
-                uint4 w = *reinterpret_cast<const uint4 *>(stage + r * 144 + c);
+                uint4 w = *reinterpret_cast<const uint4 *>(stage + row_stage_at(r, c));
                 uint4 *p = reinterpret_cast<uint4 *>(out + (size_t)r * row_bytes + c);
                 if (ELEM == 4 && accumulate) {
                     const float4 o = *reinterpret_cast<const float4 *>(p);
@@ -266,11 +281,11 @@ __device__ __forceinline__ void warp_store_rows(unsigned char *stage, int lane, 
             if (r < rows && c < bytes) {
                 char *p = out + (size_t)r * row_bytes + c;
                 if (ELEM == 4) {
-                    const float f = *reinterpret_cast<const float *>(stage + r * 144 + c);
+                    const float f = *reinterpret_cast<const float *>(stage + row_stage_at(r, c));
                     float *q = reinterpret_cast<float *>(p);
                     *q = accumulate ? *q + f : f;
                 } else {
-                    *reinterpret_cast<uint16_t *>(p) = *reinterpret_cast<const uint16_t *>(stage + r * 144 + c);
+                    *reinterpret_cast<uint16_t *>(p) = *reinterpret_cast<const uint16_t *>(stage + row_stage_at(r, c));
                 }
             }
         }

@@ -7,8 +7,15 @@
 // Three products, all by one persistent CTA-pair kernel (tcgen05, cta_group::2): a pair
 // owns a 256 x 256 tile of fp32 accumulators, each CTA its 128 rows in its own tensor
 // memory (two tiles of 256 columns: the epilogue of one tile runs under the MMAs of the
-// next).  Per K-block of 64 each CTA brings in its half of both operands (2 x 16 KB, 5
+// next).  Per K-block of 64 each CTA brings in its half of both operands (2 x 16 KB, 6
 // stages) by TMA; the leader's MMA thread issues 4 MMAs of 256 x 256 x 16.
+//   * What bounds it is those copies (about 45 B a clock and SM where a tile needs 62 at the
+//     full MMA rate), and over many calls the power limit.  Where there are tiles enough, a pair
+//     takes two neighbours at a time (WIDE: 256 x 512, both accumulators, 3 x 16 KB in 4 stages),
+//     which reads A once for both.  Their epilogues then lie between the pairs of tiles,
+//     except that the first half of the next may start while the second half of the last is
+//     read out.  In a loop: forward 8192, 4096 -> 1024 113 us (119 without), its gradient 336
+//     (350), forward 3000, 3000 -> 3000 78 (89, which also has the rounds in its favour).
 //   * gate/up: the B operand's first half is 128 gate rows (CTA 0), its second half the
 //     same 128 up rows (CTA 1), so a row's g and u meet in one thread's epilogue, which
 //     writes h, or (backward) reads dh and writes dg and du.  128 columns are also one
@@ -29,16 +36,18 @@
 // Few tokens: dense_rows_kernel (weights streamed once, tokens on the MMA's N side).
 #include "tq_dense_rows.cuh"
 
+#include <algorithm>
+
 namespace tq {
 
 constexpr int kPairM = 256, kPairN = 256;
-constexpr int kPairStages = 5;
+constexpr int kPairRing = 192 * 1024;   // operand stages: 6 of 32 KB, or 4 of 48 KB (wide tiles)
+constexpr int kPairStages = 6;
 constexpr int kPairThreads = 384;      // warp 0 TMA, 1 MMA (leader), 2 TMEM, 4-11 epilogue
 constexpr int kPairStageBytes = 16384;
 
 struct __align__(1024) PairSmem {
-    unsigned char a[kPairStages][kPairStageBytes];
-    unsigned char b[kPairStages][kPairStageBytes];
+    unsigned char ring[kPairRing];  // a stage: A, B, and in a wide tile the B of its second half
     unsigned char rows[8][kRowStage];
     uint64_t full[kPairStages];     // leader: both CTAs' copies of the stage
     uint64_t empty[kPairStages];    // MMA commit, in both CTAs
@@ -68,6 +77,7 @@ struct PairArgs {
     int words;                                // of dg and du: 1, 2
     __nv_bfloat16 *dx, *dwg, *dwu;            // [T][D], [F][D], [F][D]
     // tile plan (plan_gateup, plan_grads)
+    int wide;                                 // tiles of 512 columns, counted as two of 256 each
     long long full;                           // gate/up: whole tiles; the others are halved
     long long tiles;                          // gate/up: tiles, halves counted one by one
     int halved;                               // gradients: every tile is half as wide
@@ -91,10 +101,22 @@ struct PairTile {
 };
 
 // The j-th tile of a pair; false past its last.
-template <int KIND>
+template <int KIND, bool WIDE>
 __device__ __forceinline__ bool pair_tile(const PairArgs &p, long long pair, long long pairs, long long j, PairTile &r) {
     int m, n;
     if (KIND != kPairGrads) {
+        if (WIDE) {
+            const long long t = pair + (j >> 1) * pairs;
+            if (t >= p.tiles) return false;
+            grouped_tile(t, (p.T + kPairM - 1) / kPairM, (p.F + 255) / 256, m, n);
+            r.m0 = m * kPairM;
+            r.n0 = n * 256 + 128 * (int)(j & 1);
+            r.width = 256;
+            r.kblocks = (p.D + 63) / 64;
+            r.which = -1;
+            r.k0 = r.part = 0;
+            return true;
+        }
         // whole tiles first, then the halves of the last ones
         long long t = pair + j * pairs;
         if (t >= p.tiles) return false;
@@ -110,8 +132,9 @@ __device__ __forceinline__ bool pair_tile(const PairArgs &p, long long pair, lon
         r.k0 = r.part = 0;
         return true;
     }
-    r.width = p.halved ? 128 : 256;
-    const int nd = (p.D + r.width - 1) / r.width, mf = (p.F + kPairM - 1) / kPairM;
+    const int width = WIDE ? 512 : p.halved ? 128 : 256, second = WIDE ? (int)(j & 1) : 0;
+    if (WIDE) j >>= 1;
+    const int nd = (p.D + width - 1) / width, mf = (p.F + kPairM - 1) / kPairM;
     const bool more = pair < p.more;
     const long long dw = p.n_dw / pairs + (more ? 1 : 0);
     long long t;
@@ -138,7 +161,8 @@ __device__ __forceinline__ bool pair_tile(const PairArgs &p, long long pair, lon
         r.m0 = m * kPairM;
         k = 2 * ((p.F + 63) / 64);
     }
-    r.n0 = n * r.width;
+    r.width = p.halved ? 128 : 256;
+    r.n0 = n * width + 256 * second;
     r.k0 = (int)((long long)k * r.part / split);
     r.kblocks = (int)((long long)k * (r.part + 1) / split) - r.k0;
     return true;
@@ -224,6 +248,7 @@ __device__ __forceinline__ void store_outputs(const PairArgs &p, const PairTile 
 template <int KIND>
 __device__ __forceinline__ void pair_epilogue(const PairArgs &p, const PairTile &t, uint32_t taddr, int row0, int lane,
                                               int w, unsigned char *stage) {
+    if (t.n0 >= (KIND == kPairGrads ? p.D : p.F)) return;     // a wide tile's second half past the matrix
     uint32_t a[32], b[32];
     float v[32];
     uint4 o[8];
@@ -307,7 +332,7 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs &p, const PairTile 
 
 // ------------------------------------------------------------------------------ kernel
 
-template <int KIND>
+template <int KIND, bool WIDE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     pair_gemm_kernel(const __grid_constant__ PairMaps maps, const PairArgs args) {
     extern __shared__ __align__(128) unsigned char smem_raw[];
@@ -345,10 +370,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         return ok;
     };
 
+    constexpr bool wide = WIDE;
+    constexpr uint32_t stages = wide ? 4 : 6, stage_bytes = (wide ? 3 : 2) * kPairStageBytes;
     if (warp == 0) {
         if (lane == 0) {
             bool ok = true;
-            uint32_t it = 0;
+            uint32_t s = 0, turn = 0, it = 0;         // stage, and how often the ring was filled
             // operand tile of 64 or 128 rows x 64 K in 64 x 64 boxes: K-major (rows then K)
             // or MN-major (K rows of 64 consecutive matrix columns)
             auto load = [&](unsigned char *dst, const CUtensorMap *m, int r0, int k0, bool mn, bool two, uint32_t bar) {
@@ -356,80 +383,124 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                 if (two) tma_load_2d_pair(dst + 8192, m, mn ? r0 + 64 : k0, mn ? k0 : r0 + 64, bar);
             };
             PairTile tl;
-            for (long long j = 0; ok && pair_tile<KIND>(args, pair, pairs, j, tl); ++j) {
+            for (long long j = 0; ok && pair_tile<KIND, WIDE>(args, pair, pairs, j, tl); j += 1 + wide) {
                 const bool two = tl.width == 256;         // B rows of a CTA: 128, or 64
                 const int nb = tl.n0 + (tl.width / 2) * rank;
-                const uint32_t bytes = 2 * (kPairStageBytes + (two ? kPairStageBytes : kPairStageBytes / 2));
+                const uint32_t bytes =
+                    2 * (wide ? 3 * kPairStageBytes : kPairStageBytes + (two ? kPairStageBytes : kPairStageBytes / 2));
                 // dx: K-blocks of dg, then of du; dw: of the tokens, then again for the second word
                 const int half = (args.F + 63) / 64, tokens = (args.T + 63) / 64;
                 for (int kb = tl.k0; kb < tl.k0 + tl.kblocks; ++kb, ++it) {
-                    const int s = it % kPairStages;
-                    if (it >= kPairStages && !wait(&sm.empty[s], (it / kPairStages - 1) & 1)) {
+                    if (turn > 0 && !wait(&sm.empty[s], (turn - 1) & 1)) {
                         ok = false;
                         break;
                     }
+                    unsigned char *a = sm.ring + s * stage_bytes, *b = a + kPairStageBytes, *b2 = b + kPairStageBytes;
                     const uint32_t bar = map_to_rank(smem_u32(&sm.full[s]), 0);
                     if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], bytes);
                     const int ar = tl.m0 + 128 * rank;
                     if (KIND != kPairGrads) {
-                        load(sm.a[s], &maps.a0, ar, kb * 64, false, true, bar);
-                        load(sm.b[s], rank ? &maps.b1 : &maps.b0, tl.n0, kb * 64, false, two, bar);
+                        const CUtensorMap *w = rank ? &maps.b1 : &maps.b0;
+                        load(a, &maps.a0, ar, kb * 64, false, true, bar);
+                        load(b, w, tl.n0, kb * 64, false, two, bar);
+                        if (wide) load(b2, w, tl.n0 + 128, kb * 64, false, true, bar);
                     } else if (tl.which >= 0) {
                         const bool lo = kb >= tokens;
                         const int k0 = (lo ? kb - tokens : kb) * 64;
-                        load(sm.a[s], tl.which ? (lo ? &maps.a1_lo : &maps.a1) : (lo ? &maps.a0_lo : &maps.a0), ar, k0,
-                             true, true, bar);
-                        load(sm.b[s], &maps.x, nb, k0, true, two, bar);
+                        load(a, tl.which ? (lo ? &maps.a1_lo : &maps.a1) : (lo ? &maps.a0_lo : &maps.a0), ar, k0, true,
+                             true, bar);
+                        load(b, &maps.x, nb, k0, true, two, bar);
+                        if (wide) load(b2, &maps.x, nb + 256, k0, true, true, bar);
                     } else {
                         const bool up = kb >= half;
                         const int k0 = (up ? kb - half : kb) * 64;
-                        load(sm.a[s], up ? &maps.a1 : &maps.a0, ar, k0, false, true, bar);
-                        load(sm.b[s], up ? &maps.b1 : &maps.b0, nb, k0, true, two, bar);
+                        const CUtensorMap *w = up ? &maps.b1 : &maps.b0;
+                        load(a, up ? &maps.a1 : &maps.a0, ar, k0, false, true, bar);
+                        load(b, w, nb, k0, true, two, bar);
+                        if (wide) load(b2, w, nb + 256, k0, true, true, bar);
+                    }
+                    if (++s == stages) {
+                        s = 0;
+                        ++turn;
                     }
                 }
             }
             // every stage read by its MMAs before the CTA can exit; after a wait that gave
             // up, time for the copies in flight to land
-            for (uint32_t i = it > kPairStages ? it - kPairStages : 0; i < it && ok; ++i)
-                ok = wait(&sm.empty[i % kPairStages], (i / kPairStages) & 1);
+            for (uint32_t i = it > stages ? it - stages : 0; i < it && ok; ++i)
+                ok = wait(&sm.empty[i % stages], (i / stages) & 1);
             if (!ok)
                 for (int i = 0; i < 2000; ++i) __nanosleep(1000);
         }
     } else if (warp == 1) {
         if (rank == 0 && lane == 0) {
             bool ok = true;
-            uint32_t it = 0;
+            uint32_t s = 0, turn = 0;
             const int fmt = args.f16 ? 0 : 1;
             PairTile tl;
-            for (uint32_t j = 0; ok && pair_tile<KIND>(args, pair, pairs, j, tl); ++j) {
+            for (uint32_t j = 0; ok && pair_tile<KIND, WIDE>(args, pair, pairs, j, tl); j += 1 + wide) {
                 const bool a_mn = KIND == kPairGrads && tl.which >= 0, b_mn = KIND == kPairGrads;
                 const uint32_t idesc = umma_idesc(kPairM, tl.width, fmt, a_mn, b_mn);
-                const uint32_t st = j & 1, d = tmem + st * kPairN;
-                if (j >= 2 && !wait(&sm.acc_empty[st], ((j >> 1) - 1) & 1)) break;
+                const uint32_t a_step = a_mn ? 128 : 2, b_step = b_mn ? 128 : 2;   // 16-byte units per K = 16
+                const uint32_t st = j & 1, parity = ((j >> 1) - 1) & 1;
+                // MMAs of stage `at` into accumulator `acc`, from its B or (second) the wide tile's other
+                auto multiply = [&](uint32_t at, uint32_t acc, bool second, bool first_block) {
+                    const uint32_t as = smem_u32(sm.ring) + at * stage_bytes;
+                    const uint32_t bs = as + (second ? 2 : 1) * kPairStageBytes;
+                    const uint64_t ad = a_mn ? umma_desc_mn_sw128(as) : umma_desc_sw128(as);
+                    const uint64_t bd = b_mn ? umma_desc_mn_sw128(bs) : umma_desc_sw128(bs);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_f16_pair(tmem + acc * kPairN, ad + k * a_step, bd + k * b_step, idesc, !first_block || k != 0);
+                };
+                if (j >= 2 && !wait(&sm.acc_empty[st], parity)) break;
+                // A wide tile's second half may follow the first by the ring: its accumulator is
+                // still being read out when the first one is free.
+                bool other = !wide || j < 2;
+                int k2 = 0;                   // wide: next K-block of the second half, and its stage
+                uint32_t s2 = s;
                 tc_fence_after();
-                for (int kb = 0; kb < tl.kblocks; ++kb, ++it) {
-                    const int s = it % kPairStages;
-                    if (!wait(&sm.full[s], (it / kPairStages) & 1)) {
+                for (int kb = 0; kb < tl.kblocks; ++kb) {
+                    if (!wait(&sm.full[s], turn & 1)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t as = smem_u32(sm.a[s]), bs = smem_u32(sm.b[s]);
-                    const uint64_t ad = a_mn ? umma_desc_mn_sw128(as) : umma_desc_sw128(as);
-                    const uint64_t bd = b_mn ? umma_desc_mn_sw128(bs) : umma_desc_sw128(bs);
-                    const uint32_t a_step = a_mn ? 128 : 2, b_step = b_mn ? 128 : 2;   // 16-byte units per K = 16
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        umma_f16_pair(d, ad + k * a_step, bd + k * b_step, idesc, (kb | k) != 0);
-                    umma_commit_pair(&sm.empty[s]);
+                    multiply(s, st, false, kb == 0);
+                    if (!wide) {
+                        umma_commit_pair(&sm.empty[s]);
+                    } else {
+                        const bool last = kb + 1 == tl.kblocks;
+                        if (last) umma_commit_pair(&sm.acc_full[st]);
+                        if (!other) {
+                            other = mbar_test(&sm.acc_empty[st ^ 1], parity);
+                            if (!other && (last || kb + 1 - k2 == (int)stages)) {
+                                if (!wait(&sm.acc_empty[st ^ 1], parity)) {
+                                    ok = false;
+                                    break;
+                                }
+                                other = true;
+                            }
+                            if (other) tc_fence_after();
+                        }
+                        for (; other && k2 <= kb; ++k2) {
+                            multiply(s2, st ^ 1, true, k2 == 0);
+                            umma_commit_pair(&sm.empty[s2]);
+                            if (++s2 == stages) s2 = 0;
+                        }
+                    }
+                    if (++s == stages) {
+                        s = 0;
+                        ++turn;
+                    }
                 }
-                if (ok) umma_commit_pair(&sm.acc_full[st]);
+                if (ok) umma_commit_pair(&sm.acc_full[wide ? st ^ 1 : st]);
             }
         }
     } else if (warp >= 4) {
         const int q = warp & 3, w = (warp - 4) >> 2;
         PairTile tl;
-        for (uint32_t j = 0; pair_tile<KIND>(args, pair, pairs, j, tl); ++j) {
+        for (uint32_t j = 0; pair_tile<KIND, WIDE>(args, pair, pairs, j, tl); ++j) {
             const uint32_t st = j & 1;
             const bool ok = __all_sync(0xffffffffu, wait(&sm.acc_full[st], (j >> 1) & 1));
             if (!ok) break;
@@ -561,7 +632,8 @@ constexpr double kTwoWordsMost = 512.0 * 1024 * 1024;
 // Estimated times of plan_grads in us: a K-block of 64 in a whole and a halved tile (whose MMAs take
 // half as long; the copies' latency is the same), a piece's start and end, the launch that adds
 // partial sums, and the bytes it moves in one.
-constexpr double kBlockUs = 0.35, kHalfBlockUs = 0.30, kPieceUs = 1.0, kReduceUs = 3.0, kReduceBytesUs = 4e6;
+constexpr double kBlockUs = 0.35, kHalfBlockUs = 0.30, kWideBlockUs = 0.60, kPieceUs = 1.0, kWidePieceUs = 4.0,
+                 kTileEndUs = 2.0, kReduceUs = 3.0, kReduceBytesUs = 4e6;
 
 static int pair_map(CUtensorMap *m, const void *base, long long rows, long long cols, int f16) {
     return matrix_map(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, rows, cols,
@@ -574,8 +646,16 @@ static int pair_map(CUtensorMap *m, const void *base, long long rows, long long 
 // as 68 halves.  It pays where there are few rounds (1111 tokens, 1000 -> 504, 20 tiles as 40: the
 // gradient's two launches 25.6 -> 20.6 us); over several rounds the power limit gives the time back.
 static long long plan_gateup(PairArgs &p, long long pairs, bool may_halve) {
-    const long long n = (((long long)p.T + kPairM - 1) / kPairM) * ((p.F + 127LL) / 128), last = n % pairs;
-    p.full = may_halve && 2 * last <= pairs ? n - last : n;
+    const long long mt = ((long long)p.T + kPairM - 1) / kPairM;
+    const long long n = mt * ((p.F + 127LL) / 128), last = n % pairs, n2 = mt * ((p.F + 255LL) / 256);
+    const bool halve = may_halve && 2 * last <= pairs;
+    const double kb = (p.D + 63) / 64;
+    const double t = std::max(kb * kBlockUs, kTileEndUs), t_half = std::max(kb * kHalfBlockUs, kTileEndUs);
+    const double t_wide = std::max(kb * kWideBlockUs + 0.5 * kWidePieceUs, 2 * kTileEndUs);
+    const double narrow = (double)(n / pairs) * t + (last == 0 ? 0 : halve ? t_half : t);
+    p.wide = (double)((n2 + pairs - 1) / pairs) * t_wide < narrow;
+    if (p.wide) return p.tiles = n2;
+    p.full = halve ? n - last : n;
     p.tiles = p.full + 2 * (n - p.full);
     return p.tiles;
 }
@@ -592,16 +672,17 @@ static void plan_grads(PairArgs &p, long long pairs) {
     p.words = (double)p.T * p.D * p.F <= kTwoWordsMost ? 2 : 1;
     const long long k_dw = p.words * (((long long)p.T + 63) / 64), k_dx = 2 * (((long long)p.F + 63) / 64);
     double best = -1;
-    for (int halved = 0; halved < 2; ++halved) {
-        const long long width = halved ? 128 : 256, nd = (p.D + width - 1) / width;
-        const double t_kb = halved ? kHalfBlockUs : kBlockUs;
+    for (int mode = 0; mode < 3; ++mode) {                 // whole, halved, wide
+        const long long width = mode == 2 ? 512 : mode ? 128 : 256, nd = (p.D + width - 1) / width;
+        const double t_kb = mode == 2 ? kWideBlockUs : mode ? kHalfBlockUs : kBlockUs;
+        const double t_piece = mode == 2 ? kWidePieceUs : kPieceUs;
         for (int s_dw = 1; s_dw <= 16 && (s_dw == 1 || s_dw * 4 <= k_dw); s_dw *= 2)
             for (int s_dx = 1; s_dx <= 16 && (s_dx == 1 || s_dx * 4 <= k_dx); s_dx *= 2) {
                 const long long n_dw = 2 * mf * nd * s_dw, n_dx = mt * nd * s_dx;
                 // a split is for few tiles: no more pieces than pairs
                 if ((s_dw > 1 && n_dw > pairs) || (s_dx > 1 && n_dx > 2 * pairs)) continue;
-                const double u_dw = (double)((k_dw + s_dw - 1) / s_dw) * t_kb + kPieceUs;
-                const double u_dx = (double)((k_dx + s_dx - 1) / s_dx) * t_kb + kPieceUs;
+                const double u_dw = (double)((k_dw + s_dw - 1) / s_dw) * t_kb + t_piece;
+                const double u_dx = (double)((k_dx + s_dx - 1) / s_dx) * t_kb + t_piece;
                 const long long on = n_dw + n_dx < pairs ? n_dw + n_dx : pairs;      // pairs at work
                 const long long q = n_dw / on, more = n_dw % on, rest = on - more;
                 // dx pieces of a pair with q + 1 dw pieces: a, of the others: b.  Level loads are
@@ -625,7 +706,8 @@ static void plan_grads(PairArgs &p, long long pairs) {
                 if (sums > 0) cost += kReduceUs + 8 * sums / kReduceBytesUs;
                 if (best < 0 || cost < best) {
                     best = cost;
-                    p.halved = halved;
+                    p.halved = mode == 1;
+                    p.wide = mode == 2;
                     p.split_dw = s_dw;
                     p.split_dx = s_dx;
                     p.n_dw = n_dw;
@@ -651,9 +733,16 @@ static int launch_pair(const PairMaps &maps, PairArgs p, cudaStream_t s, int sta
     const long long tiles = KIND == kPairGrads ? p.n_dw + p.n_dx : plan_gateup(p, pairs, KIND != kPairSave);
     const unsigned grid = 2 * (unsigned)(tiles < pairs ? tiles : pairs);
     LaunchScope ls(s, stage);
-    if (launch_chained(pair_gemm_kernel<KIND>, dim3(grid), dim3(kPairThreads), smem, s, maps, p) != cudaSuccess)
+    auto kernel = p.wide ? pair_gemm_kernel<KIND, true> : pair_gemm_kernel<KIND, false>;
+    if (launch_chained(kernel, dim3(grid), dim3(kPairThreads), smem, s, maps, p) != cudaSuccess)
         return record_cuda_error("pair_gemm_kernel");
     return launch_status();
+}
+
+template <int KIND>
+static bool set_pair_smem() {
+    const int smem = (int)sizeof(PairSmem) + 1024;
+    return set_smem(pair_gemm_kernel<KIND, false>, smem) || set_smem(pair_gemm_kernel<KIND, true>, smem);
 }
 
 // The first call of an entry point on a device sets up every kernel that a later call of it may
@@ -661,9 +750,8 @@ static int launch_pair(const PairMaps &maps, PairArgs p, cudaStream_t s, int sta
 static int configure_swiglu() {
     static PerDeviceFlag configured;
     if (configured.get()) return TQ_OK;
-    const int smem = (int)sizeof(PairSmem) + 1024;
-    if (set_smem(pair_gemm_kernel<kPairForward>, smem) || set_smem(pair_gemm_kernel<kPairSave>, smem) ||
-        set_smem(pair_gemm_kernel<kPairRecompute>, smem) || set_smem(pair_gemm_kernel<kPairRecomputeTwo>, smem) || set_smem(pair_gemm_kernel<kPairGrads>, smem) ||
+    if (set_pair_smem<kPairForward>() || set_pair_smem<kPairSave>() ||
+        set_pair_smem<kPairRecompute>() || set_pair_smem<kPairRecomputeTwo>() || set_pair_smem<kPairGrads>() ||
         configure_rows<16, kSwiglu>() || configure_rows<32, kSwiglu>() || configure_rows<64, kSwiglu>() ||
         configure_rows<128, kSwiglu>() || set_smem(swiglu_saved_kernel, 0) || set_smem(grads_reduce_kernel, 0) || configure_store())
         return record_cuda_error("configure_swiglu");
