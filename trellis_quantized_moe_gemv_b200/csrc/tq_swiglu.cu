@@ -640,11 +640,11 @@ static int pair_map(CUtensorMap *m, const void *base, long long rows, long long 
                       64);
 }
 
-// Gate/up tiles: where the last round over the pairs would leave half of them or more without
-// work, its tiles are halved in width (not where they store 8-bit blocks, which need all
-// 128 columns).  8192 tokens, 4096 -> 1024: 256 tiles on 74 pairs are 3 rounds and 34 tiles, run
-// as 68 halves.  It pays where there are few rounds (1111 tokens, 1000 -> 504, 20 tiles as 40: the
-// gradient's two launches 25.6 -> 20.6 us); over several rounds the power limit gives the time back.
+// Gate/up tiles, by estimated time: taken two at a time (8192 tokens, 4096 -> 1024: 128 double tiles,
+// 2 rounds of 74 pairs, 113 us in a loop; 119 one by one), or one by one, where the tiles of a last round
+// that leaves half of the pairs or more without work are halved in width (not where they store
+// 8-bit blocks, which need all 128 columns; 1111 tokens, 1000 -> 504, 20 tiles as 40: the gradient's
+// two launches 25.6 -> 20.6 us).
 static long long plan_gateup(PairArgs &p, long long pairs, bool may_halve) {
     const long long mt = ((long long)p.T + kPairM - 1) / kPairM;
     const long long n = mt * ((p.F + 127LL) / 128), last = n % pairs, n2 = mt * ((p.F + 255LL) / 256);
@@ -750,10 +750,10 @@ static bool set_pair_smem() {
 static int configure_swiglu() {
     static PerDeviceFlag configured;
     if (configured.get()) return TQ_OK;
-    if (set_pair_smem<kPairForward>() || set_pair_smem<kPairSave>() ||
-        set_pair_smem<kPairRecompute>() || set_pair_smem<kPairRecomputeTwo>() || set_pair_smem<kPairGrads>() ||
-        configure_rows<16, kSwiglu>() || configure_rows<32, kSwiglu>() || configure_rows<64, kSwiglu>() ||
-        configure_rows<128, kSwiglu>() || set_smem(swiglu_saved_kernel, 0) || set_smem(grads_reduce_kernel, 0) || configure_store())
+    if (set_pair_smem<kPairForward>() || set_pair_smem<kPairSave>() || set_pair_smem<kPairRecompute>() ||
+        set_pair_smem<kPairRecomputeTwo>() || set_pair_smem<kPairGrads>() || configure_rows<16, kSwiglu>() ||
+        configure_rows<32, kSwiglu>() || configure_rows<64, kSwiglu>() || configure_rows<128, kSwiglu>() ||
+        set_smem(swiglu_saved_kernel, 0) || set_smem(grads_reduce_kernel, 0) || configure_store())
         return record_cuda_error("configure_swiglu");
     configured.set();
     return TQ_OK;
