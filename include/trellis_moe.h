@@ -308,6 +308,8 @@ int trellis_encode(const float *target, int K, int rows, int cols, uint32_t *bit
  * The dense expert: the gated feed-forward block and the 8-bit product of an expert that
  * every token uses, next to the routed ones (no counterpart on the pages, whose subject is
  * the routed experts).  Matrices are row-major and packed; a weight is [outputs][inputs].
+ * Outputs overlap neither inputs nor each other, and a workspace (or a tq_swiglu_saved) belongs to
+ * one call at a time: calls that may run at once, on two streams or in two graphs, take their own.
  *
  * fp8_block_quantize -- x stored as E4M3 with one scale for each block of block_rows x 128
  * values (block_rows 1: rows of activations; 128: weights).  Blocks start at multiples of
