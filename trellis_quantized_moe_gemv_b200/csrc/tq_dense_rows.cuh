@@ -283,7 +283,12 @@ __global__ void __launch_bounds__(kRowsThreads, KIND != kSwiglu && N > 64 ? 1 : 
                     if (i + 1 < nkb) next = (mine ? sx[i + 1] : 0.f) * sw[i + 1];
                     asm volatile("bar.sync 1, 128;" ::: "memory");
                 }
-                const bool ok = __all_sync(0xffffffffu, wait(&sm.acc_full[st], (i / SH::kAccStages) & 1));
+                // The token scales come from the storing warps' own stores, which the MMA's commit
+                // does not order: their barrier does (looked at under the MMAs of the block).
+                bool got = true;
+                if (KIND == kFp8Store) got = wait(&sm.stored[i], 0);
+                got = got && wait(&sm.acc_full[st], (i / SH::kAccStages) & 1);
+                const bool ok = __all_sync(0xffffffffu, got);
                 if (ok) {
                     tc_fence_after();
 #pragma unroll
