@@ -15,6 +15,7 @@ from typing import List, Optional
 
 import numpy as np
 import torch
+from torch.autograd import forward_ad
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libtrellis_moe.so")
@@ -417,28 +418,48 @@ def _here(t) -> int:
 # The checks below decide the usual case in one expression and look for the reason only where it
 # fails: they are a good part of a call that takes a few microseconds.
 
-def _require_dense(t, dtype, shape, name, dev):
-    """A contiguous CUDA tensor of this dtype and shape on device `dev`, the current one."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.get_device() == dev
-            and t.shape == shape and t.is_contiguous()):
+def _require_no_history(t, name):
+    """The dense-expert calls read and write raw memory and record nothing for autograd, so a
+    derivative that is asked for through t would be lost without a word: refused."""
+    if not isinstance(t, torch.Tensor):
         return
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError("%s requires a gradient, and this call records no history for autograd: call it under "
+                         "torch.no_grad() or on %s.detach(), and swiglu_backward for a SwiGLU block's gradients"
+                         % (name, name))
+    if forward_ad._current_level >= 0 and forward_ad.unpack_dual(t).tangent is not None:
+        raise ValueError("%s carries a forward-mode tangent, which this call does not propagate" % name)
+
+
+def _require_dense(t, dtype, shape, name, dev):
+    """A contiguous CUDA tensor of this dtype and shape on device `dev`, the current one, through
+    which no derivative is asked for."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.get_device() == dev
+            and t.shape == shape and t.is_contiguous() and not t.requires_grad and forward_ad._current_level < 0):
+        return
+    _require_no_history(t, name)
     _require(t, dtype, name)
     if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
-    raise ValueError("%s is on %s, but the current device is cuda:%d" % (name, t.device, dev))
+    if t.get_device() != dev:
+        raise ValueError("%s is on %s, but the current device is cuda:%d" % (name, t.device, dev))
 
 
 def _require_matrix(t, dtype, name, dev):
-    """The shape of a contiguous matrix on device `dev`, the current one."""
+    """The shape of a contiguous matrix on device `dev`, the current one, through which no
+    derivative is asked for."""
     if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.get_device() == dev
-            and t.dim() == 2 and t.is_contiguous()):
+            and t.dim() == 2 and t.is_contiguous() and not t.requires_grad and forward_ad._current_level < 0):
         return t.shape
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)
     if t.dim() != 2:
         raise ValueError("%s must be a matrix, got %d dimensions" % (name, t.dim()))
+    _require_no_history(t, name)
     _require(t, dtype, name)
-    raise ValueError("%s is on %s, but the current device is cuda:%d" % (name, t.device, dev))
+    if t.get_device() != dev:
+        raise ValueError("%s is on %s, but the current device is cuda:%d" % (name, t.device, dev))
+    return t.shape
 
 
 # The current stream's handle on a device.
@@ -617,7 +638,8 @@ def swiglu_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, ou
                    saved: Optional[SwigluSaved] = None, stream=None) -> torch.Tensor:
     """h = silu(x w_gate^T) * (x w_up^T): x [T, D], w_gate and w_up [F, D], all bf16 or all
     fp16, D and F multiples of 8; h [T, F].  `saved` receives x and the two projections in
-    8 bits for swiglu_backward."""
+    8 bits for swiglu_backward.  Nothing is recorded for autograd: as in every call of the dense
+    expert, tensors that require a gradient are refused while gradients are enabled."""
     dt, dev, dtype = _float_dtype(x, "x"), _here(x), x.dtype
     T, D = _require_matrix(x, dtype, "x", dev)
     shape = _require_matrix(w_gate, dtype, "w_gate", dev)
