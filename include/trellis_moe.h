@@ -320,8 +320,8 @@ int trellis_encode(const float *target, int K, int rows, int cols, uint32_t *bit
  *   x      : [rows][cols] of x_dtype (F16, BF16 or F32), 16-byte aligned.
  *   out    : [rows][cols] E4M3 bytes.  scales : [ceil(rows / block_rows)][ceil(cols / 128)]
  *            fp32.  Both 16-byte aligned.
- *   cols % 8 == 0; block_rows is 1 or 128.
- * fp8_block_dequantize -- out = q * scale in fp32, rounded once to out_dtype.
+ *   cols % 8 == 0; block_rows is 1 or 128.  cols up to 2^25 - 512 (block_rows 128: 2^31 - 1024).
+ * fp8_block_dequantize -- out = q * scale in fp32, rounded once to out_dtype; cols up to 2^25 - 512.
  */
 int fp8_block_quantize(const void *x, int x_dtype, int64_t rows, int cols, int block_rows, uint8_t *out,
                        float *scales, tq_stream stream);
@@ -336,10 +336,10 @@ int fp8_block_dequantize(const uint8_t *q, const float *scales, int64_t rows, in
  *   x : [M][K] E4M3, s_x : [M][ceil(K / 128)] fp32.
  *   w : [N][K] E4M3, s_w : [ceil(N / 128)][ceil(K / 128)] fp32.
  *   y : [M][N] of y_dtype (F16, BF16 or F32); accumulate != 0 (F32 only): y += the product.
- *   K % 16 == 0; M and N any size (up to 2^31 - 1024); all arrays 16-byte aligned; y overlaps
- *   no input.
- * fp8_block_linear -- the same from activations x [M][K] of x_dtype (F16, BF16 or F32),
- * which are quantised as fp8_block_quantize (block_rows 1) does on the way.  ws: device
+ *   K % 16 == 0; M and N any size (each size up to 2^31 - 1024); all arrays 16-byte aligned; y
+ *   overlaps no input.
+ * fp8_block_linear -- the same from activations x [M][K] (K up to 2^25 - 512) of x_dtype (F16, BF16
+ * or F32), which are quantised as fp8_block_quantize (block_rows 1) does on the way.  ws: device
  * workspace of fp8_block_linear_workspace_size(M, N, K) bytes, 16-byte aligned; 0 bytes (ws
  * may be NULL) for products of few rows (up to 16), which one kernel quantises and multiplies.
  * The size depends on the device's SM count: query it on the device that runs the call.
@@ -369,8 +369,8 @@ typedef struct {
  * swiglu_forward -- h = silu(g) * u with g = x W_gate^T, u = x W_up^T, in one kernel (fp32
  * sums; g and u are not rounded, h once).
  *   x : [T][D], w_gate, w_up : [F][D], h : [T][F], all of dtype (F16 or BF16), 16-byte
- *   aligned.  D % 8 == 0, F % 8 == 0 (each size up to 2^31 - 1024).  Outputs overlap no input and not
- *   each other.
+ *   aligned.  D % 8 == 0, F % 8 == 0, both from 8 to 2^25 - 512; T up to 2^31 - 1024.  Outputs overlap
+ *   no input and not each other.
  *   saved: NULL, or the arrays that receive x, g and u in 8 bits (g and u are stored from
  *   their fp32 sums by the same kernel); h is the same either way up to the order of its sums.
  */

@@ -759,9 +759,14 @@ static int configure_swiglu() {
     return TQ_OK;
 }
 
+// Largest D and F.  Byte counts of a row's rest, (D - column) * 4, are 32-bit; a wait for an accumulator
+// covers the whole of K, which at 0.6 us a K-block stays below a second here (a bounded wait gives up
+// after four); and 65535 groups of 512 columns is what the 8-bit row kernels' grid holds.
+constexpr int kMostFeatures = 65535 * 512;
+
 static int swiglu_shape_status(int T, int D, int F) {
     if (T < 0 || D < 1 || F < 1 || D % 8 || F % 8) return TQ_ERR_INVALID_ARG;
-    if (T > kMostSize || D > kMostSize || F > kMostSize) return TQ_ERR_UNSUPPORTED;
+    if (T > kMostSize || D > kMostFeatures || F > kMostFeatures) return TQ_ERR_UNSUPPORTED;
     return TQ_OK;
 }
 
