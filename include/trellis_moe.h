@@ -398,6 +398,15 @@ int swiglu_backward(const void *dh, const void *x, const tq_swiglu_saved *saved,
                     const void *w_up, int dtype, int T, int D, int F, void *dx, void *dw_gate, void *dw_up,
                     void *ws, size_t ws_bytes, tq_stream stream);
 
+/*
+ * swiglu_backward_plan -- how the current device would lay out swiglu_backward at these sizes
+ * (tracing, and tests that have to reach a layout): plan[0] bf16 words of dg and du in the weight
+ * gradients' products; plan[1] columns of a gradient tile: 128, 256, or 512 (two of 256 at a time);
+ * plan[2] and plan[3] pieces that K is cut into for the weight gradients and for dx; plan[4] columns
+ * of the tile that computes g and u again, counting both, likewise.
+ */
+int swiglu_backward_plan(int T, int D, int F, int32_t *plan);
+
 /* One width group of a layer: experts of one K, concatenated in ascending global id. */
 typedef struct {
     int K;                       /* 2, 3 or 4 bits per weight                          */

@@ -41,3 +41,13 @@ def test_rows_in_8_bits_up_to_their_limit(lib):
         assert lib.fp8_block_quantize(MISALIGNED, BF16, 1, cols, 1, FAKE, FAKE, None) == want
         assert lib.fp8_block_dequantize(MISALIGNED, FAKE, 1, cols, 1, FAKE, BF16, None) == want
     assert lib.fp8_block_quantize(MISALIGNED, BF16, 1, MOST + 8, 128, FAKE, FAKE, None) == ALIGNMENT
+
+
+def test_plan_query(lib):
+    plan = (ctypes.c_int32 * 5)()
+    assert lib.swiglu_backward_plan(3, 100, 72, plan) == 1 and lib.swiglu_backward_plan(0, 128, 72, plan) == 1
+    assert lib.swiglu_backward_plan(3, 128, 72, None) == 1
+    assert lib.swiglu_backward_plan(3, MOST + 8, 72, plan) == UNSUPPORTED
+    assert lib.swiglu_backward_plan(3, 128, 72, plan) == 0
+    words, tile, split_dw, split_dx, gateup = plan
+    assert words == 2 and tile in (128, 256, 512) and gateup in (128, 256, 512) and split_dw >= 1 and split_dx >= 1

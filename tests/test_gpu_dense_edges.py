@@ -58,3 +58,118 @@ def test_one_launch_product_uses_the_scales_of_its_own_tokens(api, M, N, K):
         got = [api.fp8_block_linear(x, w, s_w, out_dtype=F32) for x in xs]
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+# ----------------------------------------------------------------------------- gradient layouts
+
+def whole(shape, g, most):
+    return torch.randint(-most, most + 1, shape, generator=g).float()
+
+
+def exact_block(T, D, F, seed, most_dh, gate):
+    """A SwiGLU block whose every sum is a whole number.  x has a column of ones that W_gate alone
+    reads, so g = `gate` (>= 52: s = 1 / (1 + e^-g) is 1 in fp32), h = g u, dg = dh u and du = g dh;
+    each row of W_up holds two values +-2, so |u| <= 12, which 8 bits hold exactly next to x <= 3."""
+    g = torch.Generator().manual_seed(seed)
+    x, dh = whole((T, D), g, 3), whole((T, F), g, most_dh)
+    x[:, 0] = 1.0
+    a, b = torch.zeros(F, D), torch.zeros(F, D)
+    a[:, 0] = gate
+    for _ in range(2):
+        at = torch.randint(1, D, (F,), generator=g)
+        b[torch.arange(F), at] = torch.randint(0, 2, (F,), generator=g).float() * 4 - 2
+    return [t.to(BF16).cuda() for t in (x, a, b, dh)]
+
+
+def rounded(v):
+    """float64 whole numbers as fp32 (exact below 2^24), then bf16: one rounding, to even."""
+    return v.float().to(BF16)
+
+
+def check_gradients(api, x, a, b, dh, words, must_differ):
+    """Both forms of the gradient against the exact sums rounded once.  dx is taken from the first
+    bf16 words of dg and du; the weight gradients from `words` of them."""
+    T, D = x.shape
+    F = a.shape[0]
+    X, A, B, DH = (v.double() for v in (x, a, b, dh))
+    g, u = X @ A.t(), X @ B.t()
+    dg, du = DH * u, DH * g
+    first = [v.to(F32).to(BF16).double() for v in (dg, du)]
+    # dg and du fit two words, and every partial sum an fp32 significand
+    for v, w in zip((dg, du), first):
+        assert torch.equal((v - w).to(F32).to(BF16).double(), v - w)
+    unit = 4.0 if bool((du % 4 == 0).all()) else 1.0
+    assert float((dg.abs().t() @ X.abs()).max()) < 2 ** 24 and float((du.abs().t() @ X.abs()).max()) < unit * 2 ** 24
+    assert float((first[0].abs() @ A.abs() + first[1].abs() @ B.abs()).max()) < unit * 2 ** 24
+    used = (dg, du) if words == 2 else first
+    want = [rounded(first[0] @ A + first[1] @ B), rounded(used[0].t() @ X), rounded(used[1].t() @ X)]
+    if must_differ:      # the test would see a second word that is missing
+        assert not torch.equal(want[1], rounded(first[0].t() @ X)) and not torch.equal(want[2], rounded(first[1].t() @ X))
+    saved = api.SwigluSaved(T, D, F)
+    h = api.swiglu_forward(x, a, b, saved=saved)
+    assert torch.equal(h, rounded(g * u))
+    assert torch.equal(api.swiglu_forward(x, a, b), h)
+    for kw in (dict(x=x), dict(saved=saved)):
+        bufs = [torch.full((n + 1, D), 5.0, dtype=BF16, device="cuda") for n in (T, F, F)]
+        got = api.swiglu_backward(dh, a, b, dx=bufs[0][:T], dw_gate=bufs[1][:F], dw_up=bufs[2][:F], **kw)
+        for name, y, w in zip(("dx", "dw_gate", "dw_up"), got, want):
+            assert torch.equal(y, w), (name, sorted(kw))
+        assert all(bool((v[-1] == 5.0).all()) for v in bufs)
+
+
+# sizes, and the layout (148 SMs) that they are here for
+LAYOUTS = [
+    # tiles taken two at a time: whole, the last one with and without columns in its second half
+    ((2130, 1024, 1096), dict(words=1, tile=512, split_dw=1, split_dx=1)),
+    ((1629, 1296, 784), dict(words=1, tile=512, split_dw=1, split_dx=1)),
+    ((1373, 1576, 672), dict(words=1, tile=512, split_dw=1, split_dx=1)),
+    # and with K of dx in pieces
+    ((1626, 512, 3144), dict(words=1, tile=512, split_dw=1, split_dx=4)),
+    ((1615, 264, 3120), dict(words=1, tile=512, split_dw=1, split_dx=4)),
+    ((2069, 560, 2064), dict(words=1, tile=512, split_dw=1, split_dx=2)),
+    ((1577, 1328, 5576), dict(words=1, tile=512, split_dw=1, split_dx=4)),
+    # projections taken two at a time, the last one with and without columns in its second half
+    ((281, 1296, 7184), dict(words=1, tile=256, split_dw=1, split_dx=4, gateup_tile=512)),
+    ((258, 1432, 7840), dict(words=1, tile=256, split_dw=1, split_dx=4, gateup_tile=512)),
+    # halved and whole tiles, K of either kind in pieces
+    ((2154, 760, 328), dict(words=1, tile=128, split_dw=1, split_dx=1)),
+    ((1330, 304, 1328), dict(words=1, tile=128, split_dw=1, split_dx=2)),
+    ((3217, 552, 304), dict(words=1, tile=128, split_dw=2, split_dx=1)),
+    ((1773, 128, 2392), dict(words=1, tile=128, split_dw=2, split_dx=4)),
+    ((452, 3536, 336), dict(words=1, tile=256, split_dw=1, split_dx=1)),
+    ((109, 2960, 1664), dict(words=1, tile=256, split_dw=1, split_dx=4)),
+    ((5826, 240, 384), dict(words=1, tile=256, split_dw=8, split_dx=1)),
+    ((4449, 136, 888), dict(words=1, tile=256, split_dw=4, split_dx=2)),
+]
+
+
+@pytest.mark.parametrize("shape,plan", LAYOUTS)
+def test_every_layout_of_the_gradients_is_exact_on_whole_numbers(api, shape, plan):
+    chosen = api.swiglu_backward_plan(*shape)
+    assert plan == {k: chosen[k] for k in plan}
+    x, a, b, dh = exact_block(*shape, 5, 2, 64.0)
+    check_gradients(api, x, a, b, dh, 1, False)
+
+
+TWO_WORDS = [
+    ((65, 128, 72), dict(words=2, tile=128, split_dw=1, split_dx=1)),
+    ((67, 128, 480), dict(words=2, tile=128, split_dw=1, split_dx=4)),
+    ((457, 136, 64), dict(words=2, tile=128, split_dw=4, split_dx=1)),
+    ((530, 128, 208), dict(words=2, tile=128, split_dw=4, split_dx=2)),
+    ((65, 3128, 72), dict(words=2, tile=256, split_dw=1, split_dx=1)),
+    ((65, 136, 2680), dict(words=2, tile=256, split_dw=1, split_dx=16)),
+    ((2092, 136, 64), dict(words=2, tile=256, split_dw=16, split_dx=1)),
+    ((979, 152, 264), dict(words=2, tile=256, split_dw=8, split_dx=2)),
+    ((777, 1032, 392), dict(words=2, tile=128, split_dw=1, split_dx=1)),
+]
+
+
+@pytest.mark.parametrize("shape,plan", TWO_WORDS)
+def test_weight_gradients_of_small_problems_take_two_words(api, shape, plan):
+    """dg = dh u and du = 60 dh with |dh| up to 255 (63 where F is large, for sums below 2^24) need up
+    to 12 bits, four more than a bf16 word has: the weight gradients are those of both words, each
+    with the tokens it belongs to."""
+    chosen = api.swiglu_backward_plan(*shape)
+    assert plan == {k: chosen[k] for k in plan}
+    x, a, b, dh = exact_block(*shape, 6, 63 if shape[2] > 2000 else 255, 60.0)
+    check_gradients(api, x, a, b, dh, 2, True)

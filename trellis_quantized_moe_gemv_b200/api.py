@@ -94,6 +94,7 @@ SIGNATURES = {
     "fp8_block_linear": ([_VP, _I, _VP, _VP, _I, _I, _I, _VP, _I, _I, _VP, _SZ, _VP], _I),
     "swiglu_forward": ([_VP, _VP, _VP, _I, _I, _I, _I, _VP, ctypes.POINTER(TqSwigluSaved), _VP], _I),
     "swiglu_backward_workspace_size": ([_I, _I, _I, _I], _SZ),
+    "swiglu_backward_plan": ([_I, _I, _I, ctypes.POINTER(ctypes.c_int32)], _I),
     "swiglu_backward": ([_VP, _VP, ctypes.POINTER(TqSwigluSaved), _VP, _VP, _I, _I, _I, _I, _VP, _VP, _VP, _VP,
                          _SZ, _VP], _I),
 }
@@ -659,6 +660,15 @@ def swiglu_forward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, ou
 
 def swiglu_backward_workspace_size(T: int, D: int, F: int, from_saved: bool) -> int:
     return _fn("swiglu_backward_workspace_size")(T, D, F, from_saved)
+
+
+def swiglu_backward_plan(T: int, D: int, F: int) -> dict:
+    """How swiglu_backward is laid out at these sizes on the current device: bf16 words of dg and du,
+    columns of a gradient tile, pieces of K for the weight gradients and dx, columns of a tile of
+    the recomputed projections (128: some or all tiles halved; 512: two of 256 at a time)."""
+    plan = (ctypes.c_int32 * 5)()
+    _check(_fn("swiglu_backward_plan")(T, D, F, plan), "swiglu_backward_plan")
+    return dict(zip(("words", "tile", "split_dw", "split_dx", "gateup_tile"), plan))
 
 
 def swiglu_backward(dh: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, x: Optional[torch.Tensor] = None,

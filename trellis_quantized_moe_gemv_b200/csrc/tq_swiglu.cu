@@ -971,3 +971,22 @@ TQ_API int swiglu_backward(const void *dh, const void *x, const tq_swiglu_saved 
         return record_cuda_error("grads_reduce_kernel");
     return launch_status();
 }
+
+TQ_API int swiglu_backward_plan(int T, int D, int F, int32_t *plan) {
+    const int st = tq::swiglu_shape_status(T, D, F);
+    if (st) return st;
+    if (T == 0 || !plan) return TQ_ERR_INVALID_ARG;
+    tq::PairArgs p{};
+    p.T = T;
+    p.D = D;
+    p.F = F;
+    const long long pairs = tq::num_sms() / 2;
+    tq::plan_gateup(p, pairs, true);
+    plan[4] = p.wide ? 512 : p.full < p.tiles ? 128 : 256;
+    tq::plan_grads(p, pairs);
+    plan[0] = p.words;
+    plan[1] = p.wide ? 512 : p.halved ? 128 : 256;
+    plan[2] = p.split_dw;
+    plan[3] = p.split_dx;
+    return TQ_OK;
+}
