@@ -383,8 +383,10 @@ int swiglu_forward(const void *x, const void *w_gate, const void *w_up, int dtyp
  *   dx = dg W_gate + du W_up,  dw_gate = dg^T x,  dw_up = du^T x
  * from exactly one of x (g and u are computed again) and saved (x, g and u are the 8-bit
  * values that swiglu_forward stored; dx, dw follow from those values).  The other is NULL.
- * dg and du are rounded to bf16 for the products (for the weight gradients of small problems, T D F
- * <= 2^29, to two bf16 words); sums are fp32.  Results are written (not
+ * dg and du are rounded to bf16 for the products, which leaves a gradient 0.0022-0.0025 of its norm off
+ * (rounding the result to bf16 alone: 0.0014-0.0018).  From saved, small problems with no more tokens than
+ * outputs or so keep them in two bf16 words for the weight gradients, where the last rounding alone
+ * then remains (swiglu_backward_plan tells).  Sums are fp32.  Results are written (not
  * added), do not depend on the order of execution, and must not overlap the inputs or each
  * other.
  *   dtype: BF16 (F16: TQ_ERR_UNSUPPORTED, its range does not hold dg and du).
@@ -401,9 +403,10 @@ int swiglu_backward(const void *dh, const void *x, const tq_swiglu_saved *saved,
 /*
  * swiglu_backward_plan -- how the current device would lay out swiglu_backward at these sizes
  * (tracing, and tests that have to reach a layout): plan[0] bf16 words of dg and du in the weight
- * gradients' products; plan[1] columns of a gradient tile: 128, 256, or 512 (two of 256 at a time);
- * plan[2] and plan[3] pieces that K is cut into for the weight gradients and for dx; plan[4] columns
- * of the tile that computes g and u again, counting both, likewise.
+ * gradients' products from saved activations (from x: always 1); plan[1] columns of a gradient
+ * tile: 128, 256, or 512 (two of 256 at a time); plan[2] and plan[3] pieces that K is cut into for
+ * the weight gradients and for dx; plan[4] columns of a tile that computes g and u again, counting
+ * both, likewise.
  */
 int swiglu_backward_plan(int T, int D, int F, int32_t *plan);
 

@@ -51,3 +51,22 @@ def test_plan_query(lib):
     assert lib.swiglu_backward_plan(3, 128, 72, plan) == 0
     words, tile, split_dw, split_dx, gateup = plan
     assert words == 2 and tile in (128, 256, 512) and gateup in (128, 256, 512) and split_dw >= 1 and split_dx >= 1
+
+
+@pytest.mark.parametrize("T,D,F,words", [(3, 136, 72, 2), (500, 520, 520, 2), (65, 136, 2680, 2), (612, 400, 2928, 1),
+                                         (2900, 400, 2928, 1), (777, 1032, 392, 1), (1064, 1000, 504, 1),
+                                         (1111, 1000, 504, 1), (8192, 4096, 1024, 1)])
+def test_second_words_where_the_gradients_launch_is_no_longer_for_them(lib, T, D, F, words):
+    """148 SMs.  Where every pair has one tile at most, dw tiles of both words run over 2 ceil(T / 64)
+    blocks of K and dx tiles over 2 ceil(F / 64): with no more tokens than outputs the words are
+    free but for their own bytes, which may take a third of a microsecond."""
+    plan = (ctypes.c_int32 * 5)()
+    assert lib.swiglu_backward_plan(T, D, F, plan) == 0 and plan[0] == words
+
+
+def test_workspace_holds_what_the_form_and_its_words_need(lib):
+    size = lib.swiglu_backward_workspace_size
+    up = lambda n: (n + 255) // 256 * 256
+    for T, D, F, arrays in ((500, 520, 520, 4), (1064, 1000, 504, 2)):       # no K in pieces
+        assert size(T, D, F, 0) == arrays * up(2 * T * F)
+        assert size(T, D, F, 1) == arrays * up(2 * T * F) + up(2 * T * D)

@@ -87,8 +87,8 @@ def rounded(v):
 
 
 def check_gradients(api, x, a, b, dh, words, must_differ):
-    """Both forms of the gradient against the exact sums rounded once.  dx is taken from the first
-    bf16 words of dg and du; the weight gradients from `words` of them."""
+    """Both forms of the gradient against the exact sums rounded once.  They are taken from the first
+    bf16 words of dg and du; the weight gradients from 8-bit activations from `words` of them."""
     T, D = x.shape
     F = a.shape[0]
     X, A, B, DH = (v.double() for v in (x, a, b, dh))
@@ -101,15 +101,15 @@ def check_gradients(api, x, a, b, dh, words, must_differ):
     unit = 4.0 if bool((du % 4 == 0).all()) else 1.0
     assert float((dg.abs().t() @ X.abs()).max()) < 2 ** 24 and float((du.abs().t() @ X.abs()).max()) < unit * 2 ** 24
     assert float((first[0].abs() @ A.abs() + first[1].abs() @ B.abs()).max()) < unit * 2 ** 24
-    used = (dg, du) if words == 2 else first
-    want = [rounded(first[0] @ A + first[1] @ B), rounded(used[0].t() @ X), rounded(used[1].t() @ X)]
+    want = [rounded(first[0] @ A + first[1] @ B), rounded(first[0].t() @ X), rounded(first[1].t() @ X)]
+    want_saved = want if words == 1 else [want[0], rounded(dg.t() @ X), rounded(du.t() @ X)]
     if must_differ:      # the test would see a second word that is missing
-        assert not torch.equal(want[1], rounded(first[0].t() @ X)) and not torch.equal(want[2], rounded(first[1].t() @ X))
+        assert not torch.equal(want_saved[1], want[1]) and not torch.equal(want_saved[2], want[2])
     saved = api.SwigluSaved(T, D, F)
     h = api.swiglu_forward(x, a, b, saved=saved)
     assert torch.equal(h, rounded(g * u))
     assert torch.equal(api.swiglu_forward(x, a, b), h)
-    for kw in (dict(x=x), dict(saved=saved)):
+    for kw, want in ((dict(x=x), want), (dict(saved=saved), want_saved)):
         bufs = [torch.full((n + 1, D), 5.0, dtype=BF16, device="cuda") for n in (T, F, F)]
         got = api.swiglu_backward(dh, a, b, dx=bufs[0][:T], dw_gate=bufs[1][:F], dw_up=bufs[2][:F], **kw)
         for name, y, w in zip(("dx", "dw_gate", "dw_up"), got, want):
@@ -132,14 +132,14 @@ LAYOUTS = [
     ((281, 1296, 7184), dict(words=1, tile=256, split_dw=1, split_dx=4, gateup_tile=512)),
     ((258, 1432, 7840), dict(words=1, tile=256, split_dw=1, split_dx=4, gateup_tile=512)),
     # halved and whole tiles, K of either kind in pieces
-    ((2154, 760, 328), dict(words=1, tile=128, split_dw=1, split_dx=1)),
+    ((65, 144, 64), dict(words=1, tile=128, split_dw=1, split_dx=1)),
     ((1330, 304, 1328), dict(words=1, tile=128, split_dw=1, split_dx=2)),
-    ((3217, 552, 304), dict(words=1, tile=128, split_dw=2, split_dx=1)),
+    ((1047, 136, 64), dict(words=1, tile=128, split_dw=4, split_dx=1)),
     ((1773, 128, 2392), dict(words=1, tile=128, split_dw=2, split_dx=4)),
     ((452, 3536, 336), dict(words=1, tile=256, split_dw=1, split_dx=1)),
     ((109, 2960, 1664), dict(words=1, tile=256, split_dw=1, split_dx=4)),
-    ((5826, 240, 384), dict(words=1, tile=256, split_dw=8, split_dx=1)),
-    ((4449, 136, 888), dict(words=1, tile=256, split_dw=4, split_dx=2)),
+    ((4197, 136, 64), dict(words=1, tile=256, split_dw=16, split_dx=1)),
+    ((1805, 136, 568), dict(words=1, tile=256, split_dw=4, split_dx=2)),
 ]
 
 
@@ -151,21 +151,18 @@ def test_every_layout_of_the_gradients_is_exact_on_whole_numbers(api, shape, pla
     check_gradients(api, x, a, b, dh, 1, False)
 
 
+# two words, in tiles of either width, with K of dx whole and in pieces
 TWO_WORDS = [
     ((65, 128, 72), dict(words=2, tile=128, split_dw=1, split_dx=1)),
+    ((500, 520, 520), dict(words=2, tile=128, split_dw=1, split_dx=1)),
     ((67, 128, 480), dict(words=2, tile=128, split_dw=1, split_dx=4)),
-    ((457, 136, 64), dict(words=2, tile=128, split_dw=4, split_dx=1)),
-    ((530, 128, 208), dict(words=2, tile=128, split_dw=4, split_dx=2)),
     ((65, 3128, 72), dict(words=2, tile=256, split_dw=1, split_dx=1)),
     ((65, 136, 2680), dict(words=2, tile=256, split_dw=1, split_dx=16)),
-    ((2092, 136, 64), dict(words=2, tile=256, split_dw=16, split_dx=1)),
-    ((979, 152, 264), dict(words=2, tile=256, split_dw=8, split_dx=2)),
-    ((777, 1032, 392), dict(words=2, tile=128, split_dw=1, split_dx=1)),
 ]
 
 
 @pytest.mark.parametrize("shape,plan", TWO_WORDS)
-def test_weight_gradients_of_small_problems_take_two_words(api, shape, plan):
+def test_weight_gradients_take_two_words_where_the_layout_has_time_for_them(api, shape, plan):
     """dg = dh u and du = 60 dh with |dh| up to 255 (63 where F is large, for sums below 2^24) need up
     to 12 bits, four more than a bf16 word has: the weight gradients are those of both words, each
     with the tokens it belongs to."""

@@ -663,8 +663,8 @@ def swiglu_backward_workspace_size(T: int, D: int, F: int, from_saved: bool) -> 
 
 
 def swiglu_backward_plan(T: int, D: int, F: int) -> dict:
-    """How swiglu_backward is laid out at these sizes on the current device: bf16 words of dg and du,
-    columns of a gradient tile, pieces of K for the weight gradients and dx, columns of a tile of
+    """How swiglu_backward is laid out at these sizes on the current device: bf16 words of dg and du
+    from saved activations (from x: always one), columns of a gradient tile, pieces of K for the weight gradients and dx, columns of a tile of
     the recomputed projections (128: some or all tiles halved; 512: two of 256 at a time)."""
     plan = (ctypes.c_int32 * 5)()
     _check(_fn("swiglu_backward_plan")(T, D, F, plan), "swiglu_backward_plan")

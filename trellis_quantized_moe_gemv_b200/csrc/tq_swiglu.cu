@@ -26,12 +26,13 @@
 //     the pairs that finish early.
 // dg and du are rounded to bf16 between the two launches, because the tensor cores take 16-bit
 // operands: at most 2^-8 of each term, and as the terms' errors are independent about as much
-// of a sum as the rounding of the 16-bit gradient itself (measured against 64 bits: 0.0024 of
-// the gradients' norm, 0.0017 for the last rounding alone).  For the weight gradients, which a
-// training run adds up, small problems (kTwoWordsMost) keep the remainder as a second bf16 word
-// that K then runs over too, and are left with the last rounding; their products are shorter
-// than the call (777 tokens, 1032 -> 392: a step of 40 us either way).  At 8192 tokens, 4096 -> 1024 the
-// second word would add 100 us to 300.
+// of a sum as the rounding of the 16-bit gradient itself.  Measured against 64 bits, at every size:
+// 0.0022-0.0025 of the gradients' norm, 0.0014-0.0018 for the last rounding alone.  That alone remains of
+// a weight gradient with a second bf16 word for the remainder, that K then runs over too.  From
+// 8-bit activations small problems have it, where dw tiles wait for dx tiles anyway (second_words);
+// elsewhere it would cost up to half of the pass (from x its second pass over the tile 5.5 us: 512 tokens, 512
+// -> 512 16.5 -> 22.1 us; from 8-bit activations 1064 tokens, 1000 -> 504 16.2 -> 24.6; 8192, 4096 -> 1024 209 ->
+// 307).
 //
 // Few tokens: dense_rows_kernel (weights streamed once, tokens on the MMA's N side).
 #include "tq_dense_rows.cuh"
@@ -73,8 +74,7 @@ struct PairArgs {
     float *sg, *su;                           // [T][ceil(F / 128)]
     const __nv_bfloat16 *dh;                  // [T][F]
     __nv_bfloat16 *dg, *du;                   // [T][F]
-    __nv_bfloat16 *dg_lo, *du_lo;             // [T][F], two words
-    int words;                                // of dg and du: 1, 2
+    int words;                                // of dg and du in the weight gradients: 1, 2
     __nv_bfloat16 *dx, *dwg, *dwu;            // [T][D], [F][D], [F][D]
     // tile plan (plan_gateup, plan_grads)
     int wide;                                 // tiles of 512 columns, counted as two of 256 each
@@ -88,9 +88,7 @@ struct PairArgs {
     float *part_dw, *part_dx;                 // split: fp32 partial sums [piece][2 F][D], [piece][T][D]
 };
 
-// kPairRecompute and kPairRecomputeTwo: dg and du in one word and in two (a kernel of its own, since
-// the second word's code costs the first word's registers).
-enum PairKind { kPairForward = 0, kPairSave = 1, kPairRecompute = 2, kPairGrads = 3, kPairRecomputeTwo = 4 };
+enum PairKind { kPairForward = 0, kPairSave = 1, kPairRecompute = 2, kPairGrads = 3 };
 
 // One output tile: rows m0 .. m0 + 255 of the pair, columns n0 .. n0 + width - 1 (gate/up:
 // width / 2 outputs; width 256, or 128 for a halved tile), `which` the matrix of a weight
@@ -184,9 +182,9 @@ __device__ __forceinline__ float bf16_remainder(float v) {
     return fabsf(d) <= FLT_MAX ? d : 0.f;
 }
 
-// The h tile (WORD < 0), or word WORD of the dg and du tiles, of one warp: columns c0 .. c0 + 63 of
-// its rows, or 32 of a halved tile (the second half of o is then not stored).
-template <int WORD>
+// The h tile, or (GRADS) the dg and du tiles, of one warp: columns c0 .. c0 + 63 of its rows, or 32 of a
+// halved tile (the second half of o is then not stored).
+template <bool GRADS>
 __device__ __forceinline__ void store_outputs(const PairArgs &p, const PairTile &t, uint32_t taddr, int r0, int lane,
                                               int w, unsigned char *stage) {
     uint32_t a[32], b[32];
@@ -202,7 +200,7 @@ __device__ __forceinline__ void store_outputs(const PairArgs &p, const PairTile 
         tmem_ld32(taddr + c, a);
         tmem_ld32(taddr + u0 + c, b);
         const int col = t.n0 + c;
-        if constexpr (WORD >= 0) {
+        if constexpr (GRADS) {
             uint4 d[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -216,10 +214,6 @@ __device__ __forceinline__ void store_outputs(const PairArgs &p, const PairTile 
                 const uint32_t w2 = reinterpret_cast<const uint32_t *>(d)[i >> 1];
                 const float dh = __uint_as_float((i & 1) ? (w2 & 0xFFFF0000u) : (w2 << 16));
                 swiglu_grads(__uint_as_float(a[i]), __uint_as_float(b[i]), dh, v[i], du[i]);
-                if (WORD == 1) {
-                    v[i] = bf16_remainder(v[i]);
-                    du[i] = bf16_remainder(du[i]);
-                }
             }
             pack_row32(v, false, o + 4 * half);
             pack_row32(du, false, o2 + 4 * half);
@@ -233,11 +227,9 @@ __device__ __forceinline__ void store_outputs(const PairArgs &p, const PairTile 
     const int col = t.n0 + c0;
     const int bytes = min((p.F - col) * 2, halved ? 64 : 128);
     const size_t at = (size_t)r0 * p.F + col;
-    if constexpr (WORD >= 0) {
-        warp_store_rows<2>(stage, lane, o, reinterpret_cast<char *>((WORD == 1 ? p.dg_lo : p.dg) + at), (size_t)p.F * 2, rows,
-                           bytes, true);
-        warp_store_rows<2>(stage, lane, o2, reinterpret_cast<char *>((WORD == 1 ? p.du_lo : p.du) + at), (size_t)p.F * 2, rows,
-                           bytes, true);
+    if constexpr (GRADS) {
+        warp_store_rows<2>(stage, lane, o, reinterpret_cast<char *>(p.dg + at), (size_t)p.F * 2, rows, bytes, true);
+        warp_store_rows<2>(stage, lane, o2, reinterpret_cast<char *>(p.du + at), (size_t)p.F * 2, rows, bytes, true);
     } else {
         warp_store_rows<2>(stage, lane, o, reinterpret_cast<char *>(p.h) + at * 2, (size_t)p.F * 2, rows, bytes, true);
     }
@@ -326,8 +318,7 @@ __device__ __forceinline__ void pair_epilogue(const PairArgs &p, const PairTile 
         warp_store_rows<2>(stage, lane, o, reinterpret_cast<char *>((w ? p.u8 : p.g8) + (size_t)r0 * p.F + t.n0),
                            (size_t)p.F, rows, p.F - t.n0, p.F % 16 == 0);
     }
-    store_outputs<KIND == kPairRecompute || KIND == kPairRecomputeTwo ? 0 : -1>(p, t, taddr, r0, lane, w, stage);
-    if constexpr (KIND == kPairRecomputeTwo) store_outputs<1>(p, t, taddr, r0, lane, w, stage);
+    store_outputs<KIND == kPairRecompute>(p, t, taddr, r0, lane, w, stage);
 }
 
 // ------------------------------------------------------------------------------ kernel
@@ -626,9 +617,6 @@ __global__ void __launch_bounds__(kStoreWarps * 32) swiglu_saved_kernel(const Sa
 
 static inline size_t align256_d(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// T D F up to which the weight gradients take dg and du in two bf16 words.
-constexpr double kTwoWordsMost = 512.0 * 1024 * 1024;
-
 // Estimated times of plan_grads in us: a K-block of 64 in a whole and a halved tile (whose MMAs take
 // half as long; the copies' latency is the same), a piece's start and end, the launch that adds
 // partial sums, and the bytes it moves in one.
@@ -660,64 +648,93 @@ static long long plan_gateup(PairArgs &p, long long pairs, bool may_halve) {
     return p.tiles;
 }
 
-// Gradient tiles: the dw tiles go round the pairs first; the dx tiles then fill up, so that
-// the most loaded pair has least.  Where there are few tiles they are halved in width, and K of
-// either kind is split (dw: many tokens and a small weight; dx: few tokens and a large one): the
-// pieces' fp32 sums are then added by one more launch.  The choice is the least of the estimated
-// times.  Whole backward pass, GPU us, as chosen and in one whole piece a tile: 8192 tokens, 512 -> 256
-// 26 (dw in 8 pieces), 56; 64 tokens, 4096 -> 4096 59 (dx in 4), 85; 512 tokens, 2048 -> 2048 41 (dx in
-// 4), 48; 1111 tokens, 1000 -> 504 22 (halved), 24.
-static void plan_grads(PairArgs &p, long long pairs) {
+// Columns of a gradient tile: whole, halved, wide.
+static long long grads_width(int mode) { return mode == 2 ? 512 : mode ? 128 : 256; }
+
+// Deals the gradient pieces of one tile width and split to the pairs: the dw pieces (K over `words` bf16
+// words of dg and du) go round the pairs first; the dx pieces then fill up, so that the most loaded
+// pair has least.  Fills p's plan and returns that load (estimated us).
+static double deal_grads(PairArgs &p, long long pairs, int mode, int s_dw, int s_dx, int words) {
     const long long mf = ((long long)p.F + kPairM - 1) / kPairM, mt = ((long long)p.T + kPairM - 1) / kPairM;
-    p.words = (double)p.T * p.D * p.F <= kTwoWordsMost ? 2 : 1;
-    const long long k_dw = p.words * (((long long)p.T + 63) / 64), k_dx = 2 * (((long long)p.F + 63) / 64);
-    double best = -1;
+    const long long k_dw = words * (((long long)p.T + 63) / 64), k_dx = 2 * (((long long)p.F + 63) / 64);
+    const long long nd = (p.D + grads_width(mode) - 1) / grads_width(mode);
+    const double t_kb = mode == 2 ? kWideBlockUs : mode ? kHalfBlockUs : kBlockUs;
+    const double t_piece = mode == 2 ? kWidePieceUs : kPieceUs;
+    const long long n_dw = 2 * mf * nd * s_dw, n_dx = mt * nd * s_dx;
+    const double u_dw = (double)((k_dw + s_dw - 1) / s_dw) * t_kb + t_piece;
+    const double u_dx = (double)((k_dx + s_dx - 1) / s_dx) * t_kb + t_piece;
+    const long long on = n_dw + n_dx < pairs ? n_dw + n_dx : pairs;      // pairs at work
+    const long long q = n_dw / on, more = n_dw % on, rest = on - more;
+    // dx pieces of a pair with q + 1 dw pieces: a, of the others: b.  Level loads are
+    // at a = (n_dx u_dx / rest - u_dw) / (u_dx (1 + more / rest)); whole numbers next to it.
+    long long a = 0, b = 0;
+    double load = -1;
+    const double level = (n_dx * u_dx / rest - u_dw) / (u_dx * (1.0 + (double)more / rest));
+    const long long top = more ? (n_dx + more - 1) / more : 0, x0 = level > 1 ? (long long)level - 1 : 0;
+    for (long long x = x0 < top ? x0 : top; x <= top && x <= x0 + 3; ++x) {
+        const long long left = n_dx - more * x, y = left > 0 ? (left + rest - 1) / rest : 0;
+        const double l1 = more ? (q + 1) * u_dw + x * u_dx : 0, l0 = q * u_dw + y * u_dx;
+        const double l = l1 > l0 ? l1 : l0;
+        if (load < 0 || l < load) {
+            load = l;
+            a = x;
+            b = y;
+        }
+    }
+    p.words = words;
+    p.halved = mode == 1;
+    p.wide = mode == 2;
+    p.split_dw = s_dw;
+    p.split_dx = s_dx;
+    p.n_dw = n_dw;
+    p.n_dx = n_dx;
+    p.more = (int)more;
+    p.dx_more = a;
+    p.dx_rest = b;
+    return load;
+}
+
+// Gradient tiles.  Where there are few they are halved in width, and K of either kind is split (dw:
+// many tokens and a small weight; dx: few tokens and a large one): the pieces' fp32 sums are then
+// added by one more launch.  The choice is the least of the estimated times.  Whole backward pass, GPU
+// us, as chosen and in one whole piece a tile: 8192 tokens, 512 -> 256 26 (dw in 8 pieces), 56; 64
+// tokens, 4096 -> 4096 59 (dx in 4), 85; 512 tokens, 2048 -> 2048 41 (dx in 4), 48; 1111 tokens, 1000 ->
+// 504 22 (halved), 24.  The plan is one for one word of dg and du; returns its load.
+static double plan_grads(PairArgs &p, long long pairs) {
+    const long long mf = ((long long)p.F + kPairM - 1) / kPairM, mt = ((long long)p.T + kPairM - 1) / kPairM;
+    const long long k_dw = ((long long)p.T + 63) / 64, k_dx = 2 * (((long long)p.F + 63) / 64);
+    double best = -1, load = 0;
+    PairArgs best_plan = p;
     for (int mode = 0; mode < 3; ++mode) {                 // whole, halved, wide
-        const long long width = mode == 2 ? 512 : mode ? 128 : 256, nd = (p.D + width - 1) / width;
-        const double t_kb = mode == 2 ? kWideBlockUs : mode ? kHalfBlockUs : kBlockUs;
-        const double t_piece = mode == 2 ? kWidePieceUs : kPieceUs;
+        const long long nd = (p.D + grads_width(mode) - 1) / grads_width(mode);
         for (int s_dw = 1; s_dw <= 16 && (s_dw == 1 || s_dw * 4 <= k_dw); s_dw *= 2)
             for (int s_dx = 1; s_dx <= 16 && (s_dx == 1 || s_dx * 4 <= k_dx); s_dx *= 2) {
-                const long long n_dw = 2 * mf * nd * s_dw, n_dx = mt * nd * s_dx;
                 // a split is for few tiles: no more pieces than pairs
-                if ((s_dw > 1 && n_dw > pairs) || (s_dx > 1 && n_dx > 2 * pairs)) continue;
-                const double u_dw = (double)((k_dw + s_dw - 1) / s_dw) * t_kb + t_piece;
-                const double u_dx = (double)((k_dx + s_dx - 1) / s_dx) * t_kb + t_piece;
-                const long long on = n_dw + n_dx < pairs ? n_dw + n_dx : pairs;      // pairs at work
-                const long long q = n_dw / on, more = n_dw % on, rest = on - more;
-                // dx pieces of a pair with q + 1 dw pieces: a, of the others: b.  Level loads are
-                // at a = (n_dx u_dx / rest - u_dw) / (u_dx (1 + more / rest)); whole numbers next to it.
-                long long a = 0, b = 0;
-                double load = -1;
-                const double level = (n_dx * u_dx / rest - u_dw) / (u_dx * (1.0 + (double)more / rest));
-                const long long top = more ? (n_dx + more - 1) / more : 0, x0 = level > 1 ? (long long)level - 1 : 0;
-                for (long long x = x0 < top ? x0 : top; x <= top && x <= x0 + 3; ++x) {
-                    const long long left = n_dx - more * x, y = left > 0 ? (left + rest - 1) / rest : 0;
-                    const double l1 = more ? (q + 1) * u_dw + x * u_dx : 0, l0 = q * u_dw + y * u_dx;
-                    const double l = l1 > l0 ? l1 : l0;
-                    if (load < 0 || l < load) {
-                        load = l;
-                        a = x;
-                        b = y;
-                    }
-                }
-                double cost = load;
+                if ((s_dw > 1 && 2 * mf * nd * s_dw > pairs) || (s_dx > 1 && mt * nd * s_dx > 2 * pairs)) break;
+                const double l = deal_grads(p, pairs, mode, s_dw, s_dx, 1);
                 const double sums = (s_dw > 1 ? 2.0 * s_dw * p.F * p.D : 0) + (s_dx > 1 ? 1.0 * s_dx * p.T * p.D : 0);
-                if (sums > 0) cost += kReduceUs + 8 * sums / kReduceBytesUs;
+                const double cost = l + (sums > 0 ? kReduceUs + 8 * sums / kReduceBytesUs : 0);
                 if (best < 0 || cost < best) {
                     best = cost;
-                    p.halved = mode == 1;
-                    p.wide = mode == 2;
-                    p.split_dw = s_dw;
-                    p.split_dx = s_dx;
-                    p.n_dw = n_dw;
-                    p.n_dx = n_dx;
-                    p.more = (int)more;
-                    p.dx_more = a;
-                    p.dx_rest = b;
+                    load = l;
+                    best_plan = p;
                 }
             }
     }
+    p = best_plan;
+    return load;
+}
+
+// Whether a plan of that load has room for second words of dg and du: the launch with them ends no
+// later, but for a K-block's time, counting the words' own bytes.  p then is the plan with them.
+// Backward pass from 8-bit activations, GPU us, with them and, for a few tokens more, without: 512 -> 512
+// 12.7 (512 tokens), 11.9 (520); 1000 -> 504 14.0 (504), 13.9 (520); 1032 -> 392 14.4 (384), 12.7 (450).
+static bool second_words(PairArgs &p, long long pairs, double load) {
+    PairArgs two = p;
+    const double l = deal_grads(two, pairs, p.wide ? 2 : p.halved, p.split_dw, p.split_dx, 2);
+    if (l + 4.0 * p.T * p.F / kReduceBytesUs > load + kBlockUs) return false;
+    p = two;
+    return true;
 }
 
 // fp32 partial sums of the plan.
@@ -751,7 +768,7 @@ static int configure_swiglu() {
     static PerDeviceFlag configured;
     if (configured.get()) return TQ_OK;
     if (set_pair_smem<kPairForward>() || set_pair_smem<kPairSave>() || set_pair_smem<kPairRecompute>() ||
-        set_pair_smem<kPairRecomputeTwo>() || set_pair_smem<kPairGrads>() || configure_rows<16, kSwiglu>() ||
+        set_pair_smem<kPairGrads>() || configure_rows<16, kSwiglu>() ||
         configure_rows<32, kSwiglu>() || configure_rows<64, kSwiglu>() || configure_rows<128, kSwiglu>() ||
         set_smem(swiglu_saved_kernel, 0) || set_smem(grads_reduce_kernel, 0) || configure_store())
         return record_cuda_error("configure_swiglu");
@@ -850,9 +867,10 @@ TQ_API int swiglu_forward(const void *x, const void *w_gate, const void *w_up, i
 }
 
 namespace tq {
-// Workspace of a backward call whose plan p holds: dg, du, x as bf16 (from_saved), partial sums.
-static size_t backward_bytes(const PairArgs &p, bool from_saved) {
-    return 2 * p.words * align256_d((size_t)p.T * p.F * 2) + (from_saved ? align256_d((size_t)p.T * p.D * 2) : 0) +
+// Workspace of a backward call whose plan p holds: dg, du (with second words where `two`), x as bf16
+// (from_saved), partial sums.
+static size_t backward_bytes(const PairArgs &p, bool two, bool from_saved) {
+    return (two ? 4 : 2) * align256_d((size_t)p.T * p.F * 2) + (from_saved ? align256_d((size_t)p.T * p.D * 2) : 0) +
            grads_part_bytes(p, false) + grads_part_bytes(p, true);
 }
 }  // namespace tq
@@ -863,8 +881,9 @@ TQ_API size_t swiglu_backward_workspace_size(int T, int D, int F, int from_saved
     p.T = T;
     p.D = D;
     p.F = F;
-    tq::plan_grads(p, tq::num_sms() / 2);
-    return tq::backward_bytes(p, from_saved != 0);
+    const long long pairs = tq::num_sms() / 2;
+    const double load = tq::plan_grads(p, pairs);
+    return tq::backward_bytes(p, tq::second_words(p, pairs, load), from_saved != 0);
 }
 
 TQ_API int swiglu_backward(const void *dh, const void *x, const tq_swiglu_saved *saved, const void *w_gate,
@@ -893,8 +912,14 @@ TQ_API int swiglu_backward(const void *dh, const void *x, const tq_swiglu_saved 
     p.T = T;
     p.D = D;
     p.F = F;
-    plan_grads(p, num_sms() / 2);
-    if (!ws || ws_bytes < backward_bytes(p, saved != nullptr)) return TQ_ERR_WORKSPACE;
+    const long long pairs = num_sms() / 2;
+    const double load = plan_grads(p, pairs);
+    // the workspace is one size for both forms but for x; only the one from 8-bit activations has
+    // second words
+    PairArgs two = p;
+    const bool has_two = second_words(two, pairs, load);
+    if (!ws || ws_bytes < backward_bytes(p, has_two, saved != nullptr)) return TQ_ERR_WORKSPACE;
+    if (saved && has_two) p = two;
 
     if ((st = configure_swiglu())) return st;
     char *w = reinterpret_cast<char *>(ws);
@@ -903,10 +928,11 @@ TQ_API int swiglu_backward(const void *dh, const void *x, const tq_swiglu_saved 
     w += align256_d((size_t)T * F * 2);
     p.du = reinterpret_cast<__nv_bfloat16 *>(w);
     w += align256_d((size_t)T * F * 2);
+    __nv_bfloat16 *dg_lo = nullptr, *du_lo = nullptr;
     if (p.words == 2) {
-        p.dg_lo = reinterpret_cast<__nv_bfloat16 *>(w);
+        dg_lo = reinterpret_cast<__nv_bfloat16 *>(w);
         w += align256_d((size_t)T * F * 2);
-        p.du_lo = reinterpret_cast<__nv_bfloat16 *>(w);
+        du_lo = reinterpret_cast<__nv_bfloat16 *>(w);
         w += align256_d((size_t)T * F * 2);
     }
     p.dx = reinterpret_cast<__nv_bfloat16 *>(dx);
@@ -935,8 +961,8 @@ TQ_API int swiglu_backward(const void *dh, const void *x, const tq_swiglu_saved 
         a.x = reinterpret_cast<__nv_bfloat16 *>(x_bf16);
         a.dg = p.dg;
         a.du = p.du;
-        a.dg_lo = p.dg_lo;
-        a.du_lo = p.du_lo;
+        a.dg_lo = dg_lo;
+        a.du_lo = du_lo;
         a.T = T;
         a.D = D;
         a.F = F;
@@ -952,15 +978,14 @@ TQ_API int swiglu_backward(const void *dh, const void *x, const tq_swiglu_saved 
     } else {
         st = pair_map(&maps.a0, x, T, D, 0);
         if (st) return st;
-        st = p.words == 2 ? launch_pair<kPairRecomputeTwo>(maps, p, s, kStageSwigluGrad)
-                          : launch_pair<kPairRecompute>(maps, p, s, kStageSwigluGrad);
+        st = launch_pair<kPairRecompute>(maps, p, s, kStageSwigluGrad);
     }
     if (st) return st;
     st = pair_map(&maps.a0, p.dg, T, F, 0);
     if (!st) st = pair_map(&maps.a1, p.du, T, F, 0);
     if (!st) st = pair_map(&maps.x, xb, T, D, 0);
-    if (!st && p.words == 2) st = pair_map(&maps.a0_lo, p.dg_lo, T, F, 0);
-    if (!st && p.words == 2) st = pair_map(&maps.a1_lo, p.du_lo, T, F, 0);
+    if (!st && p.words == 2) st = pair_map(&maps.a0_lo, dg_lo, T, F, 0);
+    if (!st && p.words == 2) st = pair_map(&maps.a1_lo, du_lo, T, F, 0);
     if (!st) st = launch_pair<kPairGrads>(maps, p, s, kStageSwigluGrad);
     if (st || (!p.part_dw && !p.part_dx)) return st;
     const long long n = (p.part_dw ? 2LL * F * D : 0) + (p.part_dx ? (long long)T * D : 0);
@@ -983,7 +1008,7 @@ TQ_API int swiglu_backward_plan(int T, int D, int F, int32_t *plan) {
     const long long pairs = tq::num_sms() / 2;
     tq::plan_gateup(p, pairs, true);
     plan[4] = p.wide ? 512 : p.full < p.tiles ? 128 : 256;
-    tq::plan_grads(p, pairs);
+    tq::second_words(p, pairs, tq::plan_grads(p, pairs));
     plan[0] = p.words;
     plan[1] = p.wide ? 512 : p.halved ? 128 : 256;
     plan[2] = p.split_dw;
