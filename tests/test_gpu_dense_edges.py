@@ -170,3 +170,37 @@ def test_weight_gradients_take_two_words_where_the_layout_has_time_for_them(api,
     assert plan == {k: chosen[k] for k in plan}
     x, a, b, dh = exact_block(*shape, 6, 63 if shape[2] > 2000 else 255, 60.0)
     check_gradients(api, x, a, b, dh, 2, True)
+
+
+# ----------------------------------------------------------------------------- the gate's range
+
+@pytest.mark.parametrize("T", [2, 300])
+def test_gates_over_the_whole_range_of_the_exponential(api, T):
+    """g = -100, -99.5 ... 100 exactly, u = 1, dh = 1: h, dg and du within the documented error of the
+    fast exponential and division, (4 + 1.2 |g|) 2^-23 of s, and its flush to 0 where s < 1.2e-38."""
+    gates = torch.arange(-200, 201).float() / 2
+    F, D = 408, 16
+    gates = torch.cat([gates, torch.zeros(F - gates.numel())])
+    a, b, x = torch.zeros(F, D), torch.zeros(F, D), torch.zeros(T, D)
+    a[:, 0], b[:, 1], x[:, :2] = gates, 1.0, 1.0
+    x, a, b = (t.to(BF16).cuda() for t in (x, a, b))
+    assert torch.equal(a[:, 0].cpu().float(), gates)                  # at most 8 bits each
+    g = f64(gates)
+    s = OD.sigmoid(g)
+    off = (4 + 1.2 * np.abs(g)) * 2.0 ** -23 * s + np.where(s < 1.2e-38, s, 0.0)       # of s
+    half, tiny = torch.finfo(BF16).eps / 2, 2.0 ** -133
+    h = g * s
+    tol = np.abs(g) * off + 2.0 ** -22 * np.abs(h)                    # two fp32 products
+    got = f64(api.swiglu_forward(x, a, b))
+    assert np.all(np.abs(got - h) <= tol + half * (np.abs(h) + tol) + tiny)
+    # x = (1, 1, 0, ...): column 0 of dw_gate is the sum of dg over the tokens, column 1 of dw_up that of du
+    dh = torch.zeros(T, F, dtype=BF16, device="cuda")
+    dh[-1] = 1.0
+    _, da, db = api.swiglu_backward(dh, a, b, x=x)
+    dg, du = OD.swiglu_factor_grads(g, np.ones(F), np.ones(F))
+    # s (1 + g (1 - s)): 1 - s is off by s's error and a rounding
+    e1 = off * (1 + np.abs(g) * (1 - s)) + s * np.abs(g) * (off + 2.0 ** -23) + 2.0 ** -21 * s * (1 + np.abs(g))
+    e2 = np.abs(g) * off + 2.0 ** -22 * np.abs(du)
+    for got, want, e in ((f64(da)[:, 0], dg, e1), (f64(db)[:, 1], du, e2)):
+        e = e + half * (np.abs(want) + e) + tiny                       # dg and du in bf16
+        assert np.all(np.abs(got - want) <= e + half * (np.abs(want) + e) + tiny)

@@ -295,9 +295,11 @@ __device__ __forceinline__ void warp_store_rows(unsigned char *stage, int lane, 
 
 // ------------------------------------------------------------------------------ SwiGLU
 
-// s(z) = 1 / (1 + e^-z).  e^-z overflows to infinity below -88 and s is then 0, as its
-// limit.  The exponential and the division are CUDA's fast ones: their error (|z| 2^-24
-// of the value at most) stays far below the rounding of the 16-bit results they feed.
+// s(z) = 1 / (1 + e^-z).  The exponential and the division are CUDA's fast ones, documented as off by
+// 2 + 1.2 |z| and 2 units in the last place (2^-23): for z > 0 the exponential's share of that shrinks
+// with e^-z, for z < 0 s is off by (4 + 1.2 |z|) 2^-23 of its value, 2^-16 at z = -87.  The division is 0
+// for divisors past 2^126, so s is 0 below z = -87.3 where its value is below 1.2e-38.  Both stay far
+// below the rounding of the 16-bit results they feed (2^-12 of the value in fp16, 2^-9 in bf16).
 __device__ __forceinline__ float sigmoid_f32(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 __device__ __forceinline__ float swiglu_value(float g, float u) { return g * sigmoid_f32(g) * u; }
 
