@@ -204,3 +204,94 @@ def test_gates_over_the_whole_range_of_the_exponential(api, T):
     for got, want, e in ((f64(da)[:, 0], dg, e1), (f64(db)[:, 1], du, e2)):
         e = e + half * (np.abs(want) + e) + tiny                       # dg and du in bf16
         assert np.all(np.abs(got - want) <= e + half * (np.abs(want) + e) + tiny)
+
+
+# ----------------------------------------------------------------------------- next to the routed GEMM
+
+@pytest.mark.parametrize("T", [339, 340, 700])
+def test_dense_expert_next_to_the_routed_experts_of_a_prefill_batch(api, T):
+    """From 340 tokens on the routed part is the GEMM.  The sum is the routed result plus the dense
+    expert's, added by its FP8 product; captured, it is the same."""
+    from trellis_quantized_moe_gemv_b200 import inputs
+    layer = inputs.small_layer(31, E=12, D=256, F=128)
+    D, FS, k = 256, 336, 4
+    dl = api.DeviceLayer.from_synthetic(layer)
+    rng = np.random.default_rng(33)
+    x = torch.from_numpy(inputs.random_activations(rng, (T, D), "bf16")).to(BF16)
+    logits = torch.from_numpy(inputs.normal_logits(rng, T, 12))
+    a, b = rand((FS, D), 33, BF16, D ** -0.5), rand((FS, D), 34, BF16, D ** -0.5)
+    shared = api.SharedExpert.from_dense(a, b, rand((D, FS), 35, BF16, FS ** -0.5))
+    xd, ld = x.cuda(), logits.cuda()
+    routed = api.moe_layer(dl, xd, ld, k).clone()
+    got = api.moe_layer(dl, xd, ld, k, shared=shared).clone()
+    h = api.swiglu_forward(xd, a, b)
+    q, s = OD.quantize(f64(h))
+    y, mag = OD.block_product(q, s, f64(shared.w_down), f64(shared.s_down))
+    want = f64(routed) + y
+    assert np.all(np.abs(f64(got) - want) <= (FS + 5) * 2.0 ** -23 * (mag + np.abs(want)))
+    assert torch.equal(got, api.fp8_block_linear(h, shared.w_down, shared.s_down, out=routed, accumulate=True))
+    graph = api.MoeGraph(dl, x.pin_memory(), logits.pin_memory(), k, shared=shared)
+    out = graph.replay()
+    graph.stream.synchronize()
+    assert torch.equal(out, got.cpu())
+
+
+# ----------------------------------------------------------------------------- past 2^31 elements
+
+def test_many_rows_past_32_bit_offsets(api):
+    """h, dg, du and the 8-bit g and u have 2.2e9 elements; whole numbers, so results are exact."""
+    T, D, F = 270000, 64, 8192
+    x, a, b, dh_rows = exact_block(300, D, F, 7, 2, 64.0)
+    big = x.repeat(900, 1)
+    assert big.shape == (T, D) and T * F > 2 ** 31
+    X, A, B, DH = (v.double() for v in (x, a, b, dh_rows))
+    u = X @ B.t()
+    want = rounded(64.0 * u)
+    places = (0, 261900, 262200, T - 300)           # 2^31 / F = 262144 lies in the second
+    saved = api.SwigluSaved(T, D, F)
+    for h in (api.swiglu_forward(big, a, b), api.swiglu_forward(big, a, b, saved=saved)):
+        for r in places:
+            assert torch.equal(h[r:r + 300], want)
+        del h
+    dh = torch.zeros(T, F, dtype=BF16, device="cuda")
+    for r in places:
+        dh[r:r + 300] = dh_rows
+    dg, du = DH * u, 64.0 * DH
+    dx_want = rounded(dg @ A + du @ B)
+    n = len(places)
+    assert float((dg.abs().t() @ X.abs()).max()) * n < 2 ** 24 and float((DH.abs().t() @ X.abs()).max()) * n < 2 ** 24
+    for kw in (dict(x=big), dict(saved=saved)):
+        dx, da, db = api.swiglu_backward(dh, a, b, **kw)
+        assert torch.equal(da, rounded(n * (dg.t() @ X))) and torch.equal(db, rounded(n * (du.t() @ X)))
+        for r in places:
+            assert torch.equal(dx[r:r + 300], dx_want)
+        dx[0:300] = 0
+        for r in places:
+            dx[r:r + 300] = 0
+        assert not dx.any()
+
+
+def test_large_weights_past_32_bit_offsets(api):
+    """Weights and their gradients have 2.15e9 elements each."""
+    T, D, F = 16, 46400, 46400
+    assert D * F > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(8)
+    pick = lambda shape, most: torch.randint(-most, most + 1, shape, generator=g, device="cuda")
+    x, dh = pick((T, D), 3).to(BF16), pick((T, F), 2).to(BF16)
+    x[:, 0] = 1.0
+    a, b = torch.zeros(F, D, dtype=BF16, device="cuda"), torch.zeros(F, D, dtype=BF16, device="cuda")
+    a[:, 0] = 64.0
+    at = torch.randint(1, D, (F,), generator=g, device="cuda")
+    b[torch.arange(F, device="cuda"), at] = 2.0
+    u = 2.0 * x.double()[:, at]
+    assert torch.equal(api.swiglu_forward(x, a, b), rounded(64.0 * u))
+    dx, da, db = api.swiglu_backward(dh, a, b, x=x)
+    dg, du, X = dh.double() * u, 64.0 * dh.double(), x.double()
+    want = torch.zeros(T, D, dtype=torch.float64, device="cuda")
+    want.index_add_(1, at, 2.0 * du)
+    want[:, 0] += 64.0 * dg.sum(1)
+    assert float(dg.abs().sum(1).max()) < 2 ** 24                      # in units of 64
+    assert torch.equal(dx, rounded(want))
+    for f in (0, 20000, 46280, F - 100):                               # 2^31 / D = 46282.4
+        assert torch.equal(da[f:f + 100], rounded(dg[:, f:f + 100].t() @ X))
+        assert torch.equal(db[f:f + 100], rounded(du[:, f:f + 100].t() @ X))
