@@ -340,9 +340,10 @@ int fp8_block_dequantize(const uint8_t *q, const float *scales, int64_t rows, in
  *   overlaps no input.
  * fp8_block_linear -- the same from activations x [M][K] (K up to 2^25 - 512) of x_dtype (F16, BF16
  * or F32), which are quantised as fp8_block_quantize (block_rows 1) does on the way.  ws: device
- * workspace of fp8_block_linear_workspace_size(M, N, K) bytes, 16-byte aligned; 0 bytes (ws
- * may be NULL) for products of few rows (up to 16), which one kernel quantises and multiplies.
- * The size depends on the device's SM count: query it on the device that runs the call.
+ * workspace of fp8_block_linear_workspace_size(M, N, K) bytes, 16-byte aligned.  Only where that is 0
+ * may ws be NULL: for many, not all, products of up to 16 rows, which one kernel then quantises and
+ * multiplies (16 x 1024 x 4096: 0; 16 x 16384 x 4096: not).  The size depends on M, N, K and the
+ * device's SM count: query it on the device that runs the call.
  */
 int fp8_block_gemm(const uint8_t *x, const float *s_x, const uint8_t *w, const float *s_w, int M, int N, int K,
                    void *y, int y_dtype, int accumulate, tq_stream stream);

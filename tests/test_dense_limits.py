@@ -70,3 +70,11 @@ def test_workspace_holds_what_the_form_and_its_words_need(lib):
     for T, D, F, arrays in ((500, 520, 520, 4), (1064, 1000, 504, 2)):       # no K in pieces
         assert size(T, D, F, 0) == arrays * up(2 * T * F)
         assert size(T, D, F, 1) == arrays * up(2 * T * F) + up(2 * T * D)
+
+
+def test_products_of_few_rows_may_need_a_workspace(lib):
+    size, call = lib.fp8_block_linear_workspace_size, lib.fp8_block_linear
+    assert size(16, 1024, 4096) == 0 and size(16, 16384, 4096) > 0
+    for n in (0, size(16, 16384, 4096) - 1):
+        ws = FAKE if n else None
+        assert call(FAKE, BF16, FAKE, FAKE, 16, 16384, 4096, FAKE, BF16, 0, ws, ctypes.c_size_t(n), None) == 4
