@@ -12,7 +12,9 @@
 // fp32 accumulator in tensor memory, and while the next block's MMAs fill the other one
 // the 8 epilogue warps of each CTA add s_x s_w times it to fp32 registers (128 columns of
 // a row a thread).  Per CTA and K-block the MMAs take 512 cycles at the E4M3 rate, reading
-// 128 x 256 accumulators and as many FMAs at least 256 each on their own pipes.
+// 128 x 256 accumulators and as many FMAs at least 256 each on their own pipes.  Measured
+// (8192 x 4096 x 4096, 130 us): 1050 a K-block, 840 without the FMAs, the tensor pipe busy 47 %; both
+// accumulators fill tensor memory, so the MMAs of block k + 2 wait until all 16 warps have read block k.
 // Few rows: dense_rows_kernel.
 #include "tq_dense_rows.cuh"
 
