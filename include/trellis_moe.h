@@ -384,7 +384,7 @@ int swiglu_forward(const void *x, const void *w_gate, const void *w_up, int dtyp
  *   dx = dg W_gate + du W_up,  dw_gate = dg^T x,  dw_up = du^T x
  * from exactly one of x (g and u are computed again) and saved (x, g and u are the 8-bit
  * values that swiglu_forward stored; dx, dw follow from those values).  The other is NULL.
- * dg and du are rounded to bf16 for the products, which leaves a gradient 0.0022-0.0025 of its norm off
+ * dg and du are rounded to bf16 for the products, which leaves a gradient 0.0022-0.0026 of its norm off
  * (rounding the result to bf16 alone: 0.0014-0.0018).  From saved, small problems with no more tokens than
  * outputs or so keep them in two bf16 words for the weight gradients, where the last rounding alone
  * then remains (swiglu_backward_plan tells).  Sums are fp32.  Results are written (not

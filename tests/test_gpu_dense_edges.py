@@ -295,3 +295,99 @@ def test_large_weights_past_32_bit_offsets(api):
     for f in (0, 20000, 46280, F - 100):                               # 2^31 / D = 46282.4
         assert torch.equal(da[f:f + 100], rounded(dg[:, f:f + 100].t() @ X))
         assert torch.equal(db[f:f + 100], rounded(du[:, f:f + 100].t() @ X))
+
+
+# ----------------------------------------------------------------------------- calls at once
+
+class Step:
+    """A training step and a serving product of one stream, on buffers of their own."""
+
+    def __init__(self, api, T, D, F, seed):
+        self.api = api
+        self.x, self.dh = rand((T, D), seed, BF16), rand((T, F), seed + 1, BF16, 0.1)
+        self.a, self.b = rand((F, D), seed + 2, BF16, D ** -0.5), rand((F, D), seed + 3, BF16, D ** -0.5)
+        self.w, self.s_w = api.fp8_block_quantize(rand((D, F), seed + 4, F32, F ** -0.5), 128)
+        self.saved = api.SwigluSaved(T, D, F)
+        e = lambda *n, dtype=BF16: torch.empty(n, dtype=dtype, device="cuda")
+        self.h, self.dx, self.da, self.db, self.y = e(T, F), e(T, D), e(F, D), e(F, D), e(T, D, dtype=F32)
+        self.ws = e(max(api.swiglu_backward_workspace_size(T, D, F, s) for s in (True, False)), dtype=torch.uint8)
+        self.ws2 = e(max(api.fp8_block_linear_workspace_size(T, D, F), 16), dtype=torch.uint8)
+
+    def run(self):
+        api, grads = self.api, dict(dx=self.dx, dw_gate=self.da, dw_up=self.db, ws=self.ws)
+        api.swiglu_forward(self.x, self.a, self.b, out=self.h, saved=self.saved)
+        api.fp8_block_linear(self.h, self.w, self.s_w, out=self.y, ws=self.ws2)
+        api.swiglu_backward(self.dh, self.a, self.b, x=self.x, **grads)
+        api.swiglu_backward(self.dh, self.a, self.b, saved=self.saved, **grads)
+        api.fp8_block_linear(self.h, self.w, self.s_w, out=self.y, accumulate=True, ws=self.ws2)
+
+    def results(self):
+        return [t.clone() for t in (self.h, self.dx, self.da, self.db, self.y)]
+
+
+SIZES = [((5, 512, 1040), (700, 264, 400)), ((200, 1024, 512), (1500, 520, 1200)), ((1500, 1096, 1200), (1300, 2600, 1392))]
+
+
+@pytest.mark.parametrize("sizes", SIZES)
+def test_two_streams_at_once(api, sizes):
+    """Steps of different sizes on two streams, whose kernels run next to and behind one another, have
+    the bits that they have alone."""
+    steps = [Step(api, *s, 100 * i) for i, s in enumerate(sizes)]
+    want = []
+    for s in steps:
+        s.run()
+        torch.cuda.synchronize()
+        want.append(s.results())
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        for s in steps:
+            for t in (s.h, s.dx, s.da, s.db, s.y):
+                t.fill_(7.0)
+        torch.cuda.synchronize()
+        for _ in range(10):
+            for st, s in zip(streams, steps):
+                with torch.cuda.stream(st):
+                    s.run()
+        torch.cuda.synchronize()
+        for s, w in zip(steps, want):
+            assert all(torch.equal(a, b) for a, b in zip(s.results(), w))
+
+
+@pytest.mark.parametrize("sizes", SIZES)
+def test_two_branches_of_a_captured_graph(api, sizes):
+    """The same as two branches of one graph, forked behind a kernel that fills their inputs and
+    joined in front of one that reads their results."""
+    steps = [Step(api, *s, 100 * i + 50) for i, s in enumerate(sizes)]
+    for s in steps:
+        s.run()
+    torch.cuda.synchronize()
+    inputs = [[s.x.clone() for s in steps], [s.x * 0.5 for s in steps]]
+    want = []
+    for xs in inputs:
+        for s, x in zip(steps, xs):
+            s.x.copy_(x)
+            s.run()
+        torch.cuda.synchronize()
+        want.append([s.results() for s in steps])
+    source = [x.clone() for x in inputs[0]]
+    copies = [[torch.empty_like(t) for t in (s.h, s.dx, s.da, s.db, s.y)] for s in steps]
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        for s, x in zip(steps, source):
+            s.x.copy_(x)
+        side.wait_stream(main)
+        steps[0].run()
+        with torch.cuda.stream(side):
+            steps[1].run()
+        main.wait_stream(side)
+        for s, c in zip(steps, copies):
+            for t, o in zip((s.h, s.dx, s.da, s.db, s.y), c):
+                o.copy_(t)
+    for n in range(6):
+        for x, v in zip(source, inputs[n % 2]):
+            x.copy_(v)
+        graph.replay()
+        torch.cuda.synchronize()
+        for c, w in zip(copies, want[n % 2]):
+            assert all(torch.equal(a, b) for a, b in zip(c, w))

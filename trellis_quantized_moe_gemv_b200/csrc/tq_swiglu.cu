@@ -27,7 +27,7 @@
 // dg and du are rounded to bf16 between the two launches, because the tensor cores take 16-bit
 // operands: at most 2^-8 of each term, and as the terms' errors are independent about as much
 // of a sum as the rounding of the 16-bit gradient itself.  Measured against 64 bits, at every size:
-// 0.0022-0.0025 of the gradients' norm, 0.0014-0.0018 for the last rounding alone.  That alone remains of
+// 0.0022-0.0026 of the gradients' norm, 0.0014-0.0018 for the last rounding alone.  That alone remains of
 // a weight gradient with a second bf16 word for the remainder, that K then runs over too.  From
 // 8-bit activations small problems have it, where dw tiles wait for dx tiles anyway (second_words);
 // elsewhere it would cost up to half of the pass (from x its second pass over the tile 5.5 us: 512 tokens, 512
